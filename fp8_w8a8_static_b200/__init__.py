@@ -34,7 +34,9 @@ __all__ = [
     "qkv_shared_quant", "qkv_shared_quant_workspace", "fp8_shared_quant_linears",
     "fp8_linears_static",
     "cross_attention_qkv_static_fp8", "fp8_quant_per_token", "fp8_linear_scaled",
-    "silu_mul_2in_fp8_per_token", "gated_mlp_per_token_fp8",
+    "silu_mul_2in_fp8_per_token", "gated_mlp_per_token_fp8", "fp8_linear_epilogue",
+    "fp4_kv_cache", "fp4_kv_tables", "fp4_kv_append", "fp4_kv_gather", "fp4_kv_attention",
+    "fp4_kv_attention_workspace",
     "fp8_check_shared_input_scale", "fp8_absmax_bf16", "fp8_silu_mul_absmax",
     "fp8_observer_scale", "fp8_rtn_quantize_weight",
     "device_check", "device_status", "launch_count", "launch_log", "launch_log_clear",
@@ -59,6 +61,7 @@ OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_SCALE_MISMATCH, ERR_BAD_SCALE, ERR_CUDA,
     ERR_DEVICE_TIMEOUT, ERR_UNSUPPORTED, ERR_WORKSPACE = range(10)
 
 KIND_QUANT, KIND_GEMM, KIND_SWIGLU, KIND_CALIB, KIND_DUAL = 1, 2, 3, 4, 5
+KIND_KV_CACHE, KIND_KV_ATTENTION = 6, 7
 SITE_SELFTEST = 6  # wait site recorded by the bounded-wait self-test
 
 
@@ -162,6 +165,18 @@ _SIGS = {
     "gated_mlp_per_token_fp8_workspace": (ctypes.c_size_t, [_I64, _I64, _I64]),
     "gated_mlp_per_token_fp8": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P,
                                                _P, _P]),
+    "fp8_linear_epilogue": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, _P, _P, _P, ctypes.c_int, _P,
+                                           _P, _P, _P]),
+    "fp4_kv_tables": (ctypes.c_int, [_P, _P, _I64, ctypes.c_int, _P, _I64, _P, _I64, _P, _P, _P,
+                                     _P, _P, _I64, _P]),
+    "fp4_kv_append": (ctypes.c_int, [_P, _P, _I64, _I64, ctypes.c_int, _P, _P, _P, _P, _I64,
+                                     ctypes.c_int, _P]),
+    "fp4_kv_gather": (ctypes.c_int, [_P, _I64, ctypes.c_int, _I64, ctypes.c_int, _P, _I64, _P, _P,
+                                     _P, _P, _P]),
+    "fp4_kv_attention_workspace": (ctypes.c_size_t, []),
+    "fp4_kv_attention": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _P, _I64, _P, _I64, _P, _I64,
+                                        ctypes.c_int, _I64, ctypes.c_int, _P, _P, ctypes.c_float,
+                                        ctypes.c_int, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "fp8_check_shared_input_scale": (ctypes.c_int, [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int,
                                                     _P]),
     "fp8_absmax_bf16": (ctypes.c_int, [_P, _I64, _P, _P]),
@@ -774,6 +789,240 @@ def gated_mlp_per_token_fp8(x, wg, s_wg, wu, s_wu, wd, s_wd, workspace=None, out
             _dev_ptr(workspace, "workspace", (torch.uint8,)), _bf16(out, "out"), _stream(stream)),
             "gated_mlp_per_token_fp8")
     return out
+
+
+def _on(first, stream):
+    """(device index, raw stream) of a call on first's device."""
+    if not isinstance(first, torch.Tensor):
+        raise TypeError("expected a torch.Tensor")
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError(f"expected a CUDA tensor, got one on {first.device}")
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, _stream(stream)
+
+
+def _ptr(t, name, dev, *dtypes):
+    """_dev_ptr for a tensor that must also be on device dev (the common case
+    is five attribute reads; the messages are _dev_ptr's)."""
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype in dtypes
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _dev_ptr(t, name, dtypes)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+
+
+def _scalar(t, name, dev):
+    p = _ptr(t, name, dev, torch.float32)
+    if p == 0:
+        raise ValueError(f"{name} must hold at least one fp32 value")
+    return p
+
+
+def _call(dev, fn, name, *args):
+    """fn(*args) with dev current, its status checked."""
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args)
+    if status != OK:
+        raise FP8WSError(status, name)
+
+
+def _scratch(nbytes, dev, stream):
+    """A workspace for one call on the given stream: memory of another stream
+    than the current one is not handed out again before that stream is done."""
+    ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        ws.record_stream(stream)
+    return ws
+
+
+# ---------------------------------------- Linear with a fused epilogue
+
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
+
+
+def fp8_linear_epilogue(xq, wq, s_in, s_w, bias=None, act="none", residual=None, s_out=None,
+                        out=None, stream=None) -> torch.Tensor:
+    """act((s_in*s_w) * Xq . Wq^T + bias) + residual in one launch: BF16, or
+    with s_out E4M3 codes of the value over s_out.  bias [N], residual [M,N]
+    BF16 (residual may be out); act: "none", "relu", "silu" or "gelu" (tanh
+    form)."""
+    lib = load()
+    if xq.dim() != 2 or wq.dim() != 2 or xq.shape[1] != wq.shape[1]:
+        raise ValueError(f"shapes {tuple(xq.shape)} x {tuple(wq.shape)}^T do not match")
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
+    M, K = xq.shape
+    N = wq.shape[0]
+    if bias is not None and tuple(bias.shape) != (N,):
+        raise ValueError("bias must be [N]")
+    if residual is not None and tuple(residual.shape) != (M, N):
+        raise ValueError("residual must be [M, N]")
+    if out is not None and tuple(out.shape) != (M, N):
+        raise ValueError("out must be [M, N]")
+    dev, st = _on(xq, stream)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16 if s_out is None else FP8, device=dev)
+    bf16, u8 = torch.bfloat16, torch.uint8
+    _call(dev, lib.fp8_linear_epilogue, "fp8_linear_epilogue", _ptr(xq, "xq", dev, FP8, u8),
+          _ptr(wq, "wq", dev, FP8, u8), M, N, K, _scalar(s_in, "s_in", dev),
+          _scalar(s_w, "s_w", dev), None if bias is None else _ptr(bias, "bias", dev, bf16),
+          ACTIVATIONS[act], None if residual is None else _ptr(residual, "residual", dev, bf16),
+          None if s_out is None else _scalar(s_out, "s_out", dev),
+          _ptr(out, "out", dev, bf16) if s_out is None else _ptr(out, "out", dev, FP8, u8), st)
+    return out
+
+
+# ------------------------------------------------ attention over a 4-bit cache
+
+
+def _kv_shape(cache):
+    """(pages, kv heads, page size, head dim) of a cache tensor."""
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 4 or cache.shape[3] % 18:
+        raise ValueError("cache must be [pages, kv_heads, page_size / 16, 18 * head_dim]")
+    return cache.shape[0], cache.shape[1], 16 * cache.shape[2], cache.shape[3] // 18
+
+
+def fp4_kv_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int,
+                 device="cuda") -> torch.Tensor:
+    """An empty 4-bit K/V cache: uint8 [pages, kv_heads, page_size / 16, 18 *
+    head_dim], 4.5 bits an element (the layout is in include/fp8ws.h)."""
+    if page_size not in (16, 32, 64, 128, 256) or head_dim not in (64, 128):
+        raise ValueError("page_size must be 16, 32, 64, 128 or 256 and head_dim 64 or 128")
+    return torch.zeros((num_pages, kv_heads, page_size // 16, 18 * head_dim), dtype=torch.uint8,
+                       device=device)
+
+
+def fp4_kv_tables(lens, added, block_table, free_pages, used, page_size: int, n_slots: int,
+                  out=None, stream=None):
+    """(cu_q [B+1], kv_lens [B], slots [n_slots] int64, pool [2]) of a step in
+    which request b goes from lens[b] to lens[b] + added[b] tokens; writes the
+    new pages, taken from free_pages[used:], into block_table [B, W].  pool is
+    (used after the step, pages that were missing).  All int32 on the device;
+    out=(cu_q, kv_lens, slots, pool), where kv_lens may be lens and pool may be
+    the two-element tensor given as used."""
+    lib = load()
+    if lens.dim() != 1 or added.shape != lens.shape:
+        raise ValueError("lens and added must be [B]")
+    B = lens.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, W]")
+    if free_pages.dim() != 1:
+        raise ValueError("free_pages must be one-dimensional")
+    if used.numel() < 1:
+        raise ValueError("used must hold one value")
+    dev, st = _on(lens, stream)
+    i32, i64 = torch.int32, torch.int64
+    if out is None:
+        out = (torch.empty(B + 1, dtype=i32, device=dev), torch.empty(B, dtype=i32, device=dev),
+               torch.empty(n_slots, dtype=i64, device=dev), torch.empty(2, dtype=i32, device=dev))
+    cu_q, kv_lens, slots, pool = out
+    if (cu_q.numel() != B + 1 or kv_lens.numel() != B or slots.numel() != n_slots
+            or pool.numel() != 2):
+        raise ValueError("out must be cu_q [B+1], kv_lens [B], slots [n_slots] and pool [2]")
+    _call(dev, lib.fp4_kv_tables, "fp4_kv_tables", _ptr(lens, "lens", dev, i32),
+          _ptr(added, "added", dev, i32), B, page_size, _ptr(block_table, "block_table", dev, i32),
+          block_table.shape[1], _ptr(free_pages, "free_pages", dev, i32), free_pages.numel(),
+          _ptr(used, "used", dev, i32), _ptr(pool, "pool", dev, i32), _ptr(cu_q, "cu_q", dev, i32),
+          _ptr(kv_lens, "kv_lens", dev, i32), _ptr(slots, "slots", dev, i64), n_slots, st)
+    return out
+
+
+def fp4_kv_append(k, v, slots, cache, s_k, s_v, stream=None) -> None:
+    """Quantize k and v [T, kv_heads, head_dim] (or [T, kv_heads * head_dim],
+    as the projections give them) into the cache at slots [T] int64; a slot
+    outside the cache is skipped, the others must differ."""
+    lib = load()
+    pages, heads, page, dim = _kv_shape(cache)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [T]")
+    T = slots.shape[0]
+    for t, n in ((k, "k"), (v, "v")):
+        if tuple(t.shape) not in ((T, heads, dim), (T, heads * dim)):
+            raise ValueError(f"{n} must be [T, {heads}, {dim}] with the T of slots")
+    dev, st = _on(cache, stream)
+    _call(dev, lib.fp4_kv_append, "fp4_kv_append", _ptr(k, "k", dev, torch.bfloat16),
+          _ptr(v, "v", dev, torch.bfloat16), T, heads, dim, _ptr(slots, "slots", dev, torch.int64),
+          _scalar(s_k, "s_k", dev), _scalar(s_v, "s_v", dev),
+          _ptr(cache, "cache", dev, torch.uint8), pages, page, st)
+
+
+def fp4_kv_gather(cache, slots, s_k, s_v, out=None, stream=None):
+    """(k, v) [T, kv_heads, head_dim] BF16: the tokens at slots [T] int64 as
+    the cache holds them; zeros for a slot outside the cache."""
+    lib = load()
+    pages, heads, page, dim = _kv_shape(cache)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [T]")
+    T = slots.shape[0]
+    dev, st = _on(cache, stream)
+    bf16 = torch.bfloat16
+    if out is None:
+        out = (torch.empty((T, heads, dim), dtype=bf16, device=dev),
+               torch.empty((T, heads, dim), dtype=bf16, device=dev))
+    k, v = out
+    if k.numel() != T * heads * dim or v.numel() != T * heads * dim:
+        raise ValueError(f"out must be two tensors [T, {heads}, {dim}]")
+    _call(dev, lib.fp4_kv_gather, "fp4_kv_gather", _ptr(cache, "cache", dev, torch.uint8), pages,
+          page, heads, dim, _ptr(slots, "slots", dev, torch.int64), T, _scalar(s_k, "s_k", dev),
+          _scalar(s_v, "s_v", dev), _ptr(k, "k", dev, bf16), _ptr(v, "v", dev, bf16), st)
+    return out
+
+
+def fp4_kv_attention_workspace() -> int:
+    return load().fp4_kv_attention_workspace()
+
+
+def fp4_kv_attention(q, cu_q, kv_lens, block_table, cache, s_k, s_v, max_q: int, scale=None,
+                     causal: bool = True, s_out=None, return_lse: bool = False, workspace=None,
+                     out=None, lse=None, stream=None):
+    """Attention of packed rows q [total_q, q_heads, head_dim] BF16 over the
+    4-bit cache.  Request b owns rows cu_q[b]..cu_q[b+1]-1 and the first
+    kv_lens[b] tokens of block_table[b]; causal: its rows are its last tokens.
+    max_q: at least the most rows of a request.  scale: 1/sqrt(head_dim) by
+    default.  Returns out (BF16, or with s_out E4M3 codes of o / s_out), and
+    with return_lse also lse [total_q, q_heads] fp32 (natural logarithm).  A
+    row that sees no token gives zeros and -inf; rows outside every request are
+    left as they were."""
+    lib = load()
+    pages, heads, page, dim = _kv_shape(cache)
+    if q.dim() != 3 or q.shape[2] != dim or q.shape[1] < 1 or q.shape[1] % heads:
+        raise ValueError(f"q must be [total_q, a multiple of {heads}, {dim}]")
+    if kv_lens.dim() != 1 or tuple(cu_q.shape) != (kv_lens.shape[0] + 1,):
+        raise ValueError("kv_lens must be [B] and cu_q [B + 1]")
+    B = kv_lens.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, W]")
+    if scale is None:
+        scale = dim ** -0.5
+    if out is not None and out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is not None and lse.shape != q.shape[:2]:
+        raise ValueError("lse must be [total_q, q_heads]")
+    dev, st = _on(q, stream)
+    if workspace is None:
+        workspace = _scratch(lib.fp4_kv_attention_workspace(), dev, stream)
+    bf16, i32, u8 = torch.bfloat16, torch.int32, torch.uint8
+    if out is None:
+        out = torch.empty(q.shape, dtype=bf16 if s_out is None else FP8, device=dev)
+    if return_lse and lse is None:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+    _call(dev, lib.fp4_kv_attention, "fp4_kv_attention", _ptr(q, "q", dev, bf16), q.shape[0],
+          q.shape[1], B, _ptr(cu_q, "cu_q", dev, i32), _ptr(kv_lens, "kv_lens", dev, i32), max_q,
+          _ptr(block_table, "block_table", dev, i32), block_table.shape[1],
+          _ptr(cache, "cache", dev, u8), pages, page, heads, dim, _scalar(s_k, "s_k", dev),
+          _scalar(s_v, "s_v", dev), float(scale), int(bool(causal)),
+          None if s_out is None else _scalar(s_out, "s_out", dev),
+          _ptr(out, "out", dev, bf16) if s_out is None else _ptr(out, "out", dev, FP8, u8),
+          None if lse is None else _ptr(lse, "lse", dev, torch.float32),
+          _ptr(workspace, "workspace", dev, u8), workspace.numel(), st)
+    return (out, lse) if return_lse else out
 
 
 # ---------------------------------------------------------------- load time

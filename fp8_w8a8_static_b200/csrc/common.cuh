@@ -26,6 +26,8 @@ enum WaitSite : int {
   kSiteSelfTest = 6,  // fp8ws_selftest_bounded_wait
   kSiteStagedFull = 7,   // staged quantizer: a chunk that did not arrive
   kSiteStagedEmpty = 8,  // staged quantizer: a ring slot that was not released
+  kSiteKvRows = 9,       // attention over the 4-bit cache, few rows: strips that did not arrive
+  kSiteEpiResidual = 10, // Linear with a fused epilogue: a residual box that did not arrive
 };
 
 __device__ __forceinline__ void record_timeout(int site) {

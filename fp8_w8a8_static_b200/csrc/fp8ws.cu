@@ -19,7 +19,10 @@
 
 #include "common.cuh"
 #include "elementwise.cuh"
+#include "fp4_attention.cuh"
+#include "fp4_kv.cuh"
 #include "gemm_dual_sm100.cuh"
+#include "gemm_epilogue_sm100.cuh"
 #include "gemm_pair_sm100.cuh"
 #include "gemm_sm100.cuh"
 
@@ -49,7 +52,15 @@ void log_launch(int kind, const void *in0, const void *in1, const void *out, int
   if (member == 0) ++g_launch_total;
 }
 
-enum { kKindQuant = 1, kKindGemm = 2, kKindSwiglu = 3, kKindCalib = 4, kKindDual = 5 };
+enum {
+  kKindQuant = 1,
+  kKindGemm = 2,
+  kKindSwiglu = 3,
+  kKindCalib = 4,
+  kKindDual = 5,
+  kKindKvCache = 6,
+  kKindKvAttention = 7
+};
 
 // --------------------------------------------------------------- device info
 // Per-device state, written once under g_dev_mu and read without it: the
@@ -61,8 +72,9 @@ struct DeviceInfo {
   // bit per kernel whose attributes were set on this device: 0-2 one-CTA GEMMs,
   // 3/5/6/7 pair GEMM scale modes (+16 direct-store), 9 five-stage pair GEMM,
   // 4 dual (+8 variant, +16 direct variant, +24 direct plain), 8 per-token SwiGLU,
-  // 10 staged quantizer
-  std::atomic<unsigned> gemm_attr_set{0};
+  // 10 staged quantizer, 32-35 attention over the 4-bit cache (few rows),
+  // 36-39 Linear with a fused epilogue
+  std::atomic<uint64_t> gemm_attr_set{0};
   std::atomic<int> pair_clusters{0};  // CTA pairs of the pair GEMM resident at once
   std::atomic<int> dual_clusters{0};  // CTA pairs of the gate/up dual GEMM resident at once
   // (the same for every epilogue variant: one CTA per SM either way)
@@ -74,11 +86,11 @@ std::mutex g_dev_mu;
 // `setup` runs under g_dev_mu, and the bit is published after it succeeded.
 template <typename F>
 int once_per_device(DeviceInfo *d, int bit, F setup) {
-  if (d->gemm_attr_set.load(std::memory_order_acquire) & (1u << bit)) return 0;
+  if (d->gemm_attr_set.load(std::memory_order_acquire) & (uint64_t{1} << bit)) return 0;
   std::lock_guard<std::mutex> lk(g_dev_mu);
-  if (d->gemm_attr_set.load(std::memory_order_relaxed) & (1u << bit)) return 0;
+  if (d->gemm_attr_set.load(std::memory_order_relaxed) & (uint64_t{1} << bit)) return 0;
   const int rc = setup();
-  if (rc == 0) d->gemm_attr_set.fetch_or(1u << bit, std::memory_order_release);
+  if (rc == 0) d->gemm_attr_set.fetch_or(uint64_t{1} << bit, std::memory_order_release);
   return rc;
 }
 
@@ -895,6 +907,99 @@ int swiglu_params(const fp8ws_swiglu *act, SwigluParams *p) {
   return FP8WS_OK;
 }
 
+// ------------------------------------------- Linear with a fused epilogue
+template <bool FP8, bool RES, int BIT>
+int launch_gemm_epilogue(DeviceInfo *d, const PairProblem &q, int K, const EpilogueArgs &e,
+                         const uint16_t *residual, cudaStream_t st) {
+  using C = EpiCfg<FP8, RES>;
+  auto kern = fp8_gemm_epilogue_kernel<FP8, RES>;
+  int rc = pair_clusters(d, kern, kEpiThreads, C::SMEM_BYTES, BIT, &d->pair_clusters);
+  if (rc) return rc;
+  CUtensorMap ma, mb, mbh, mr, md;
+  constexpr CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  constexpr CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  constexpr CUtensorMapSwizzle sw64 = CU_TENSOR_MAP_SWIZZLE_64B;
+  rc = make_map_2d(&ma, u8, 1, q.a, q.M, K, kGemmBK, 128, true);
+  if (!rc) rc = make_map_2d(&mb, u8, 1, q.b, q.N, K, kGemmBK, 128, true);
+  if (!rc) rc = make_map_2d(&mbh, u8, 1, q.b, q.N, K, kGemmBK, 64, true);
+  if (!rc)
+    rc = make_map_2d(&md, FP8 ? u8 : bf16, FP8 ? 1 : 2, q.out, q.M, q.N, C::STORE_COLS, 32, false,
+                     sw64);
+  mr = md;  // not used without a residual
+  if (!rc && RES) rc = make_map_2d(&mr, bf16, 2, residual, q.M, q.N, 32, 32, true, sw64);
+  if (rc) return rc;
+  const PairGroup G = make_pair_group(&q, 1, kPairTile, kPairTile);
+  const int resident = d->pair_clusters.load(std::memory_order_relaxed);
+  const SplitPlan plan = make_split_plan(G.tiles, resident, (K + kGemmBK - 1) / kGemmBK, nullptr,
+                                         nullptr, tail_halves_enabled());
+  const int units = plan.dp_tiles + plan.split_tiles * plan.halves;
+  const int clusters = units < resident ? units : resident;
+  if (launch_ex(kern, dim3(2 * clusters), dim3(kEpiThreads), C::SMEM_BYTES, st, 2, ma, mb, mbh, mr,
+                md, G, e, K, kWaitLimitNs, plan) != cudaSuccess)
+    return FP8WS_ERR_CUDA;
+  log_launch(kKindGemm, q.a, q.b, q.out);
+  return launch_status();
+}
+
+// ------------------------------------------------------- 4-bit K/V cache
+// Tokens of a page as a shift; -1 unless a power of two of 16 .. 256.
+int page_shift(int page_size) {
+  for (int s = 4; s <= 8; ++s)
+    if (page_size == (1 << s)) return s;
+  return -1;
+}
+
+constexpr int64_t kLim31 = int64_t(1) << 31;
+
+int check_kv_cache(const uint8_t *cache, int64_t num_pages, int page_size, int64_t kv_heads,
+                   int head_dim, const float *s_k, const float *s_v) {
+  if (page_shift(page_size) < 0 || (head_dim != 64 && head_dim != 128)) return FP8WS_ERR_SHAPE;
+  if (num_pages < 0 || num_pages >= kLim31 || kv_heads < 1 || kv_heads > 65535)
+    return FP8WS_ERR_SHAPE;
+  if (!s_k || !s_v || (num_pages != 0 && !cache)) return FP8WS_ERR_NULL;
+  if (!aligned16(cache)) return FP8WS_ERR_ALIGN;
+  return FP8WS_OK;
+}
+
+// Grid of the append and gather kernels: one round of their threads where that
+// fits what the GPU holds at once, else a grid stride.
+template <auto Kern>
+int kv_grid(const DeviceInfo *d, int64_t units, int per_block) {
+  static const int resident = [] {
+    int r = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&r, Kern, kKvThreads, 0) != cudaSuccess ||
+        r < 1)
+      r = 1;
+    return r;
+  }();
+  const int64_t want = (units + per_block - 1) / per_block;
+  const int64_t cap = static_cast<int64_t>(d->sms) * resident;
+  return static_cast<int>(want < cap ? want : cap);
+}
+
+template <int D, int NT, int BIT>
+int launch_kv_rows(DeviceInfo *d, KvAttnArgs a, cudaStream_t st) {
+  using C = KvRowsCfg<D, NT>;
+  auto kern = fp4_kv_rows_kernel<D, NT>;
+  int rc = once_per_device(d, BIT, [&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) ==
+                   cudaSuccess
+               ? FP8WS_OK
+               : FP8WS_ERR_CUDA;
+  });
+  if (rc) return rc;
+  const int blocks = 3 * d->sms < kKvMaxBlocks ? 3 * d->sms : kKvMaxBlocks;
+  if (launch_ex(kern, dim3(blocks), dim3(kKvRowThreads), C::SMEM, st, 1, a, kWaitLimitNs) !=
+      cudaSuccess)
+    return FP8WS_ERR_CUDA;
+  log_launch(kKindKvAttention, a.q, a.cache.data, a.out);
+  if (launch_ex(fp4_kv_merge_kernel<D, NT>, dim3(blocks - 1), dim3(D), 0, st, 1, a, blocks) !=
+      cudaSuccess)
+    return FP8WS_ERR_CUDA;
+  log_launch(kKindKvAttention, a.part, nullptr, a.out);
+  return launch_status();
+}
+
 }  // namespace
 }  // namespace fp8ws
 
@@ -1526,6 +1631,170 @@ int gated_mlp_per_token_fp8(const uint16_t *x, int64_t M, int64_t dm, int64_t I,
   if (!rc) rc = silu_mul_2in_fp8_per_token(G, U, M, I, sh, H, stream);
   if (!rc) rc = fp8_linear_scaled(H, Wd, M, dm, I, sh, 1, s_wd, 1, y, stream);
   return rc;
+}
+
+int fp8_linear_epilogue(const uint8_t *xq, const uint8_t *wq, int64_t M, int64_t N, int64_t K,
+                        const float *s_in, const float *s_w, const uint16_t *bias, int act,
+                        const uint16_t *residual, const float *s_out, void *y, void *stream) {
+  int rc = check_gemm_args(xq, wq, M, N, K, s_in, s_w, y);
+  if (rc) return rc;
+  if (act < FP8WS_ACT_NONE || act > FP8WS_ACT_GELU) return FP8WS_ERR_SHAPE;
+  if (s_out && N % 16 != 0) return FP8WS_ERR_SHAPE;  // FP8 rows of Y must be 16-byte multiples
+  if (!aligned16(bias) || !aligned16(residual)) return FP8WS_ERR_ALIGN;
+  DeviceInfo *d;
+  rc = device_info(&d);
+  if (rc) return rc;
+  if (M == 0) return FP8WS_OK;
+  const PairProblem q{xq, wq, nullptr, y, static_cast<int>(M), static_cast<int>(N), s_in, s_w,
+                      nullptr, nullptr};
+  const EpilogueArgs e{s_in, s_w, bias, s_out, act};
+  const int k = static_cast<int>(K);
+  cudaStream_t st = as_stream(stream);
+  if (s_out)
+    return residual ? launch_gemm_epilogue<true, true, 36>(d, q, k, e, residual, st)
+                    : launch_gemm_epilogue<true, false, 37>(d, q, k, e, nullptr, st);
+  return residual ? launch_gemm_epilogue<false, true, 38>(d, q, k, e, residual, st)
+                  : launch_gemm_epilogue<false, false, 39>(d, q, k, e, nullptr, st);
+}
+
+// ------------------------------------------------------- 4-bit K/V cache
+
+int fp4_kv_tables(const int32_t *lens, const int32_t *added, int64_t batch, int page_size,
+                  int32_t *block_table, int64_t table_width, const int32_t *free_pages,
+                  int64_t n_free, const int32_t *used, int32_t *pool, int32_t *cu_q,
+                  int32_t *kv_lens, int64_t *slots, int64_t n_slots, void *stream) {
+  const int shift = page_shift(page_size);
+  if (shift < 0 || batch < 0 || batch >= kLim31 - kTableThreads || table_width < 0 ||
+      table_width >= kLim31 || n_free < 0 || n_free >= kLim31 || n_slots < 0 || n_slots >= kLim31)
+    return FP8WS_ERR_SHAPE;
+  if (!used || !pool || !cu_q || (batch != 0 && (!lens || !added || !kv_lens)) ||
+      (batch != 0 && table_width != 0 && !block_table) || (n_free != 0 && !free_pages) ||
+      (n_slots != 0 && !slots))
+    return FP8WS_ERR_NULL;
+  DeviceInfo *d;
+  int rc = device_info(&d);
+  if (rc) return rc;
+  const TableArgs a{lens,       added,  static_cast<int>(batch), shift, block_table,
+                    table_width, free_pages, n_free, used, pool, cu_q, kv_lens, slots,
+                    static_cast<int>(n_slots)};
+  // a second block pays once the slots take more than two rounds of the first
+  const int64_t want = (n_slots + 2 * kTableThreads - 1) / (2 * kTableThreads);
+  const int blocks = want < 1 ? 1 : (want < kTableMaxBlocks ? static_cast<int>(want) : kTableMaxBlocks);
+  if (launch_ex(fp4_kv_tables_kernel, dim3(blocks), dim3(kTableThreads), 0, as_stream(stream),
+                blocks, a) != cudaSuccess)
+    return FP8WS_ERR_CUDA;
+  log_launch(kKindKvCache, lens, added, slots);
+  return launch_status();
+}
+
+int fp4_kv_append(const uint16_t *k, const uint16_t *v, int64_t tokens, int64_t kv_heads,
+                  int head_dim, const int64_t *slots, const float *s_k, const float *s_v,
+                  uint8_t *cache, int64_t num_pages, int page_size, void *stream) {
+  int rc = check_kv_cache(cache, num_pages, page_size, kv_heads, head_dim, s_k, s_v);
+  if (rc) return rc;
+  if (tokens < 0 || tokens >= kLim31) return FP8WS_ERR_SHAPE;
+  if (tokens != 0 && (!k || !v || !slots)) return FP8WS_ERR_NULL;
+  if (!aligned16(k) || !aligned16(v)) return FP8WS_ERR_ALIGN;
+  DeviceInfo *d;
+  rc = device_info(&d);
+  if (rc) return rc;
+  if (tokens == 0) return FP8WS_OK;
+  const KvCache c{cache, num_pages, static_cast<int>(kv_heads), page_shift(page_size)};
+  const int64_t units = tokens * kv_heads;
+  const int per_block = kKvThreads / (head_dim / 4);
+  cudaStream_t st = as_stream(stream);
+  const cudaError_t e =
+      head_dim == 128
+          ? launch_ex(fp4_kv_append_kernel<128>,
+                      dim3(kv_grid<fp4_kv_append_kernel<128>>(d, units, per_block)),
+                      dim3(kKvThreads), 0, st, 1, k, v, slots, units, s_k, s_v, c)
+          : launch_ex(fp4_kv_append_kernel<64>,
+                      dim3(kv_grid<fp4_kv_append_kernel<64>>(d, units, per_block)),
+                      dim3(kKvThreads), 0, st, 1, k, v, slots, units, s_k, s_v, c);
+  if (e != cudaSuccess) return FP8WS_ERR_CUDA;
+  log_launch(kKindKvCache, k, v, cache);
+  return launch_status();
+}
+
+int fp4_kv_gather(const uint8_t *cache, int64_t num_pages, int page_size, int64_t kv_heads,
+                  int head_dim, const int64_t *slots, int64_t tokens, const float *s_k,
+                  const float *s_v, uint16_t *k, uint16_t *v, void *stream) {
+  int rc = check_kv_cache(cache, num_pages, page_size, kv_heads, head_dim, s_k, s_v);
+  if (rc) return rc;
+  if (tokens < 0 || tokens >= kLim31) return FP8WS_ERR_SHAPE;
+  if (tokens != 0 && (!k || !v || !slots)) return FP8WS_ERR_NULL;
+  if (!aligned16(k) || !aligned16(v)) return FP8WS_ERR_ALIGN;
+  DeviceInfo *d;
+  rc = device_info(&d);
+  if (rc) return rc;
+  if (tokens == 0) return FP8WS_OK;
+  const KvCache c{const_cast<uint8_t *>(cache), num_pages, static_cast<int>(kv_heads),
+                  page_shift(page_size)};
+  const int64_t units = tokens * kv_heads;
+  const int per_block = kKvThreads / (head_dim / 4);
+  cudaStream_t st = as_stream(stream);
+  const cudaError_t e =
+      head_dim == 128
+          ? launch_ex(fp4_kv_gather_kernel<128>,
+                      dim3(kv_grid<fp4_kv_gather_kernel<128>>(d, units, per_block)),
+                      dim3(kKvThreads), 0, st, 1, slots, units, s_k, s_v, c, k, v)
+          : launch_ex(fp4_kv_gather_kernel<64>,
+                      dim3(kv_grid<fp4_kv_gather_kernel<64>>(d, units, per_block)),
+                      dim3(kKvThreads), 0, st, 1, slots, units, s_k, s_v, c, k, v);
+  if (e != cudaSuccess) return FP8WS_ERR_CUDA;
+  log_launch(kKindKvCache, cache, slots, k);
+  return launch_status();
+}
+
+// Partial sums of two pieces per block of up to 16 rows x 128, their maxima and
+// sums, and the blocks' merge records.
+size_t fp4_kv_attention_workspace(void) {
+  return round256(static_cast<size_t>(2 * kKvMaxBlocks) * 16 * (128 + 2) * sizeof(float)) +
+         round256(kKvMaxBlocks * sizeof(int4));
+}
+
+int fp4_kv_attention(const uint16_t *q, int64_t total_q, int64_t q_heads, int64_t batch,
+                     const int32_t *cu_q, const int32_t *kv_lens, int64_t max_q,
+                     const int32_t *block_table, int64_t table_width, const uint8_t *cache,
+                     int64_t num_pages, int page_size, int64_t kv_heads, int head_dim,
+                     const float *s_k, const float *s_v, float scale, int causal,
+                     const float *s_out, void *out, float *lse, void *workspace,
+                     size_t workspace_bytes, void *stream) {
+  int rc = check_kv_cache(cache, num_pages, page_size, kv_heads, head_dim, s_k, s_v);
+  if (rc) return rc;
+  if (total_q < 0 || batch < 0 || max_q < 0 || table_width < 0 || q_heads < 1 ||
+      q_heads > 65535 || q_heads % kv_heads != 0)
+    return FP8WS_ERR_SHAPE;
+  // rows, row x head products and token counts are 32-bit in the kernels
+  if (total_q >= kLim31 || batch >= kLim31 - 64 || table_width >= kLim31 ||
+      total_q * q_heads >= kLim31 - 256 || (table_width << page_shift(page_size)) > kLim31 - 512)
+    return FP8WS_ERR_SHAPE;
+  if (!isfinite(scale)) return FP8WS_ERR_BAD_SCALE;
+  if (total_q != 0 && (!q || !out)) return FP8WS_ERR_NULL;
+  if (batch != 0 && (!cu_q || !kv_lens || (table_width != 0 && !block_table)))
+    return FP8WS_ERR_NULL;
+  if (!aligned16(q) || !aligned16(out)) return FP8WS_ERR_ALIGN;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+      workspace_bytes < fp4_kv_attention_workspace())
+    return FP8WS_ERR_WORKSPACE;
+  DeviceInfo *d;
+  rc = device_info(&d);
+  if (rc) return rc;
+  if (total_q == 0 || batch == 0 || max_q == 0) return FP8WS_OK;
+  const size_t part_bytes =
+      round256(static_cast<size_t>(2 * kKvMaxBlocks) * 16 * (128 + 2) * sizeof(float));
+  const KvAttnArgs a{q, static_cast<int>(total_q), static_cast<int>(batch),
+                     static_cast<int>(q_heads / kv_heads), cu_q, kv_lens, block_table, table_width,
+                     KvCache{const_cast<uint8_t *>(cache), num_pages, static_cast<int>(kv_heads),
+                             page_shift(page_size)},
+                     s_k, s_v, scale, causal ? 1 : 0, s_out, out, lse,
+                     static_cast<float *>(workspace),
+                     reinterpret_cast<int4 *>(static_cast<uint8_t *>(workspace) + part_bytes)};
+  const bool few = max_q * (q_heads / kv_heads) <= 8;
+  cudaStream_t st = as_stream(stream);
+  if (head_dim == 128)
+    return few ? launch_kv_rows<128, 1, 32>(d, a, st) : launch_kv_rows<128, 2, 33>(d, a, st);
+  return few ? launch_kv_rows<64, 1, 34>(d, a, st) : launch_kv_rows<64, 2, 35>(d, a, st);
 }
 
 int fp8_check_shared_input_scale(const float *const *d_scales, int n, void *stream) {

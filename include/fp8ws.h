@@ -546,6 +546,161 @@ FP8WS_API int gated_mlp_per_token_fp8(const uint16_t *x, int64_t M, int64_t d, i
                                       const float *s_wu, const uint8_t *Wd, const float *s_wd,
                                       void *workspace, uint16_t *y, void *stream);
 
+/* ------------------------------------ Linear with a fused epilogue */
+
+/*
+ * fp8_linear_epilogue -- fp8_linear_static with bias, activation and residual
+ * applied in the GEMM's epilogue, and the output in BF16 or as FP8 codes for
+ * the Linear that follows.  [PR] What changed (each Linear applies its own
+ * scale in the GEMM epilogue); a projection onto the residual stream (o_proj,
+ * down) or the first Linear of an MLP without a gate is one launch this way.
+ *
+ *   v = act( (s_in[0]*s_w[0]) * sum_k deq(xq[m,k]) * deq(wq[n,k]) + bias[n] ) + residual[m,n]
+ *   y[m,n] = bf16_RN(v)                      s_out == NULL
+ *   y[m,n] = E4M3_satRNE(v * (1/s_out[0]))   otherwise
+ *
+ * all in fp32 up to the one rounding.  act: FP8WS_ACT_NONE, _RELU, _SILU
+ * (x / (1 + e^-x)) or _GELU (the tanh form, 0.5 x (1 + tanh(sqrt(2/pi) (x +
+ * 0.044715 x^3)))), with fast exponential and reciprocal (relative error of a
+ * few 2^-22); a NaN passes through each of them.  An FP8 code may differ by
+ * one step from an exact evaluation's on values within rounding noise of a
+ * code boundary.
+ * bias: device [N] BF16, or NULL.  residual: device [M,N] BF16, row-major,
+ * contiguous, or NULL; it may be y itself (BF16 output), not overlap it
+ * otherwise.  s_out: device fp32, or NULL.  y: device [M,N] BF16, or FP8 codes.
+ * Sizes: as fp8_linear_static; N % 16 == 0 for FP8 output; act out of range:
+ * FP8WS_ERR_SHAPE.  bias and residual 16-byte aligned.
+ */
+enum { FP8WS_ACT_NONE = 0, FP8WS_ACT_RELU = 1, FP8WS_ACT_SILU = 2, FP8WS_ACT_GELU = 3 };
+FP8WS_API int fp8_linear_epilogue(const uint8_t *xq, const uint8_t *wq, int64_t M, int64_t N,
+                                  int64_t K, const float *s_in, const float *s_w,
+                                  const uint16_t *bias, int act, const uint16_t *residual,
+                                  const float *s_out, void *y, void *stream);
+
+/* --------------------------------------------- attention over a 4-bit cache
+ *
+ * What lies between the Q/K/V projections (qkv_shared_quant,
+ * cross_attention_qkv_static_fp8) and o_proj in a decoder that keeps its keys
+ * and values: a paged cache in 4 bits an element, the call that lays out its
+ * pages for a step, the call that stores a step's K and V, and the attention
+ * that reads it.  [BLOG] Make it fit via quantization: memory decides what
+ * runs on one GPU; the pages do not quantize the cache, the format is this
+ * library's.
+ *
+ * Cache: device, uint8 [num_pages][kv_heads][page_size / 16][18 * head_dim],
+ * 16-byte aligned.  16 tokens of one head ("a strip") are
+ *   K codes [16][D/2] | V codes [16][D/2] | K scales [16][D/16] | V scales [16][D/16]
+ * with D = head_dim.  Codes are E2M1 (sign, 2 exponent bits with bias 1, 1
+ * mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6), element 2i in the low nibble of
+ * byte i; a scale is one E4M3 code for 16 elements.  With s the static scale
+ * of K (s_k) or V (s_v), device fp32, finite and > 0 (calibrate it as max|x| /
+ * 2688, so that the largest element of all is 6 * 448 * s):
+ *   scale = E4M3_satRNE( max16 |x| / fl32(6 s) )            (IEEE fp32 division)
+ *   code  = E2M1_satRNE( x / fl32(scale * s) ), 0 where the divisor is 0
+ *   value = code * scale * s
+ * An infinity is stored as the largest value.  A NaN in a token's K or V makes
+ * that head's K scales of the token NaN, so that rows which attend to it give
+ * NaN and rows which do not are untouched.
+ * head_dim: 64 or 128.  page_size: 16, 32, 64, 128 or 256 tokens.  kv_heads:
+ * 1..65535.  FP8WS_ERR_SHAPE otherwise.
+ * A slot is a token's place in the cache: page * page_size + offset.
+ */
+
+/*
+ * fp4_kv_tables -- block tables, row offsets and slots of one serving step,
+ * on the device, from the requests' lengths alone (one launch; capturable).
+ *
+ * Request b has lens[b] tokens in the cache and gets added[b] more (negative
+ * values count as 0).  Pages are taken in request order from free_pages, from
+ * index used[0] on:
+ *   kv_lens[b] = lens[b] + added[b]
+ *   cu_q[0..batch] = running sums of added, from 0
+ *   block_table[b][j] = the next free page, for every j from ceil(lens[b] /
+ *     page_size) to ceil(kv_lens[b] / page_size) - 1; other entries stay as
+ *     they are
+ *   slots[cu_q[b] + i] = slot of token lens[b] + i of request b, for i <
+ *     added[b]; -1 for the places behind the last request (a padded batch)
+ *   pool[0] = used[0] + pages taken; pool[1] = pages wanted but not to be had
+ * Where free_pages runs out, or the table row is too short, the page is -1 and
+ * so are its tokens' slots: the calls below skip them, and pool[1] (or kv_lens
+ * against the row's capacity) tells.
+ * lens, added: device [batch] int32.  block_table: device [batch][table_width]
+ * int32.  free_pages: device [n_free] int32.  used: device int32.  pool: device
+ * int32[2].  cu_q: device int32[batch + 1].  kv_lens: device [batch] int32.
+ * slots: device [n_slots] int64 (written whole).  pool may be used, and kv_lens
+ * may be lens (advance in place); no other two may overlap.  batch, table_width,
+ * n_free, n_slots: 0 .. 2^31 - 1 (batch a little less); pointers of empty
+ * arrays may be NULL.  Sums saturate at 2^31 - 1.
+ */
+FP8WS_API int fp4_kv_tables(const int32_t *lens, const int32_t *added, int64_t batch,
+                            int page_size, int32_t *block_table, int64_t table_width,
+                            const int32_t *free_pages, int64_t n_free, const int32_t *used,
+                            int32_t *pool, int32_t *cu_q, int32_t *kv_lens, int64_t *slots,
+                            int64_t n_slots, void *stream);
+
+/*
+ * fp4_kv_append -- quantize K and V of `tokens` tokens into the cache.
+ * k, v: device [tokens][kv_heads][head_dim] BF16, contiguous (the K and V
+ * projections' outputs).  slots: device [tokens] int64; a slot outside the
+ * cache (-1, say) is skipped.  Slots must differ from one another: of two
+ * tokens with one slot, parts of either may be stored.
+ */
+FP8WS_API int fp4_kv_append(const uint16_t *k, const uint16_t *v, int64_t tokens,
+                            int64_t kv_heads, int head_dim, const int64_t *slots,
+                            const float *s_k, const float *s_v, uint8_t *cache,
+                            int64_t num_pages, int page_size, void *stream);
+
+/*
+ * fp4_kv_gather -- read tokens of the cache back as BF16: bf16(fl32(code *
+ * scale * s)), zeros for a slot outside the cache.  Slots may repeat.
+ */
+FP8WS_API int fp4_kv_gather(const uint8_t *cache, int64_t num_pages, int page_size,
+                            int64_t kv_heads, int head_dim, const int64_t *slots,
+                            int64_t tokens, const float *s_k, const float *s_v, uint16_t *k,
+                            uint16_t *v, void *stream);
+
+/*
+ * fp4_kv_attention -- attention of packed query rows over the cache.
+ *
+ *   o[i,h] = sum_j p_j v[j],  p = softmax_j( scale * q[i,h] . k[j] ),
+ *   lse[i,h] = log( sum_j exp( scale * q[i,h] . k[j] ) )
+ *
+ * Request b owns rows cu_q[b] .. cu_q[b+1] - 1 of q and the first kv_lens[b]
+ * tokens of its block table row; with causal != 0 row i of its n rows sees the
+ * tokens j <= kv_lens[b] - n + i (its rows are the context's last n tokens),
+ * else all of them.  Query head h reads K/V head h / (q_heads / kv_heads).
+ * A row that sees no token gives zeros, and lse -inf.  Rows before cu_q[0] and
+ * behind cu_q[batch] (a padded batch) are left as they were.
+ * Scores, maxima, sums and outputs are held in fp32; q enters the product as
+ * FP16 times a power of two of its row (exact for elements above 2^-24 of the
+ * row's largest), the cache's code * scale is exact in FP16, and the softmax
+ * weights are rounded to FP16 (2^-11 of each weight) for the second product.
+ * q: device [total_q][q_heads][head_dim] BF16.  cu_q: device int32[batch + 1],
+ * not decreasing.  kv_lens: device int32[batch].  max_q: at least the largest
+ * number of rows of a request (it chooses the kernels; 0 launches nothing).
+ * block_table: device [batch][table_width] int32; tokens of a page that the
+ * cache does not have (-1, say) are not read and count as not seen.  Lengths
+ * are bounded by the row's capacity, offsets by total_q.
+ * s_out NULL: out [total_q][q_heads][head_dim] BF16.  Else out holds FP8 codes
+ * E4M3_satRNE(o / s_out[0]) (to within one step, as silu_mul_2in_fp8), o_proj's
+ * input at its calibrated scale.  lse: device [total_q][q_heads] fp32, or NULL.
+ * workspace: device, fp4_kv_attention_workspace() bytes, 256-byte aligned,
+ * overwritten; calls that may overlap on the GPU need one each.
+ * The result does not depend on timing (no atomics): the same call gives the
+ * same bits.
+ * Sizes: q_heads a multiple of kv_heads, at most 65535; total_q * q_heads and
+ * table_width * page_size below 2^31 - 512.  scale finite (FP8WS_ERR_BAD_SCALE).
+ */
+FP8WS_API size_t fp4_kv_attention_workspace(void);
+FP8WS_API int fp4_kv_attention(const uint16_t *q, int64_t total_q, int64_t q_heads,
+                               int64_t batch, const int32_t *cu_q, const int32_t *kv_lens,
+                               int64_t max_q, const int32_t *block_table, int64_t table_width,
+                               const uint8_t *cache, int64_t num_pages, int page_size,
+                               int64_t kv_heads, int head_dim, const float *s_k,
+                               const float *s_v, float scale, int causal, const float *s_out,
+                               void *out, float *lse, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
 /* ------------------------------------------------------------- load time */
 
 /*
@@ -597,7 +752,8 @@ FP8WS_API int fp8ws_device_check(void);
  * GEMMs 1 (producer, free stage), 2 (MMA, loaded stage), 3 (MMA, free
  * accumulator), 4 (epilogue, finished accumulator), 5 (teardown, last MMAs);
  * 6 the self-test below; in the staged quantizer 7 (consumers, loaded chunk),
- * 8 (producer, free slot). */
+ * 8 (producer, free slot); 9 attention over the 4-bit cache (strips of the
+ * cache), 10 the Linear with a fused epilogue (a residual box). */
 FP8WS_API int fp8ws_device_status(int *status, int *where);
 
 /* Self-test of the bounded waits every GEMM kernel uses (failure detection
@@ -657,7 +813,8 @@ FP8WS_API int fp8ws_split_plan(int tiles, int pairs, int num_kb, int has_scratch
 
 /* Launch log.  Every kernel the library enqueues is counted and recorded in a
  * small ring (the most recent FP8WS_LOG_CAPACITY records).  kind: 1 quant,
- * 2 GEMM, 3 SwiGLU-quant, 4 calibration, 5 fused gate/up SwiGLU-quant.
+ * 2 GEMM, 3 SwiGLU-quant, 4 calibration, 5 fused gate/up SwiGLU-quant, 6 K/V
+ * cache (tables, append, gather), 7 attention.
  * in0/in1 are the primary input pointers (for a GEMM: activation and weight),
  * out the output pointer.  A grouped launch writes one record per problem,
  * member 0, 1, ... in group order, and counts as one launch. */
