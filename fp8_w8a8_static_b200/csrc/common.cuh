@@ -126,6 +126,25 @@ __device__ __forceinline__ bool mbar_wait_bounded_warp(uint64_t *bar, uint32_t p
   }
 }
 
+// The same wait for loops that wait often and briefly: the clock, a slow read,
+// is looked at only after 256 polls.
+__device__ __forceinline__ bool mbar_wait_polled_warp(uint64_t *bar, uint32_t parity,
+                                                      volatile int *abort, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t spins = 1;; ++spins) {
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+    if ((spins & 255u) == 0) {
+      int give_up = 0;
+      if ((threadIdx.x & 31) == 0) {
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        give_up = (*abort != 0) || (now - t0 > limit_ns);
+      }
+      if (__shfl_sync(0xFFFFFFFFu, give_up, 0)) return false;
+    }
+  }
+}
+
 // Bring `bytes` bytes at p (16-byte aligned, a multiple of 16) into L2
 // without reading them into the SM.  L2 is the point of coherence, so a
 // prefetch issued before the data's producer has finished cannot make a later

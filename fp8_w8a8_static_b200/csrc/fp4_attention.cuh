@@ -30,16 +30,25 @@
 #include "elementwise.cuh"
 #include "fp4_kv.cuh"
 
+#include <type_traits>
+
 namespace fp8ws {
 
-constexpr int kKvRowWarps = 4;
-constexpr int kKvRowThreads = kKvRowWarps * 32;
+constexpr int kKvRowWarps = 4;                             // consumers
+constexpr int kKvRowThreads = (kKvRowWarps + 1) * 32;      // and one producer warp
 constexpr int kKvChunk = 64;     // tokens of a unit
-constexpr int kKvStages = 2;     // ring slots of a warp, up to 4 strips each
+constexpr int kKvSlots = 12;     // ring slots of a block, up to 2 strips each
 constexpr int kKvMaxBlocks = 444;  // ranges at most: 148 SMs x 3 blocks
+// Blocks of an SM: 16 query rows take the registers of two (168 spill).
+__host__ __device__ constexpr int kv_blocks_per_sm(int NT) { return NT == 1 ? 3 : 2; }
 // p = 2^(s - m) may exceed 1 by this many powers of two before the running
 // maximum m is moved: FP16 holds 2^15, the sums are fp32
 constexpr float kKvSlack = 10.0f;
+
+__device__ __forceinline__ uint32_t scaled(uint32_t h, __half2 s) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&h), s);
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
 
 struct KvAttnArgs {
   const uint16_t *q;
@@ -80,14 +89,20 @@ __device__ __forceinline__ int kv_limit(const KvRequest &r, int i, int causal) {
   return causal ? min(max(r.kv - r.q_len + i + 1, 0), r.kv) : r.kv;
 }
 
-// Units (64-token chunks, one at least so that rows without tokens are
-// written too) of a request's row tiles over all heads.
+// What a segment costs beside its chunks (its queries' loads, the warps' sums),
+// in chunks: with ranges cut by chunks alone, the blocks that got many short
+// requests ended last (attend 48 requests of 17 to 6000 tokens: 67 us).
+constexpr int kKvSegmentCost = 2;
+
+// Units of a request's row tiles over all heads: 64-token chunks (one at
+// least, so that rows without tokens are written too) and the fixed cost,
+// whose units come first.
 template <int ROWS>
 __device__ __forceinline__ int64_t kv_units(const KvAttnArgs &a, int b, int &tiles, int &chunks) {
   const KvRequest r = kv_request(a, b);
   tiles = static_cast<int>((static_cast<int64_t>(r.q_len) * a.group + ROWS - 1) / ROWS);
   chunks = max(1, (r.kv + kKvChunk - 1) / kKvChunk);
-  return static_cast<int64_t>(tiles) * a.cache.heads * chunks;
+  return static_cast<int64_t>(tiles) * a.cache.heads * (chunks + kKvSegmentCost);
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -105,47 +120,121 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
   return r;
 }
 
+// (a & 0x0F0F0F0F) | (b & 0xF0F0F0F0)
+__device__ __forceinline__ uint32_t low_high_nibbles(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xCA;" : "=r"(r) : "r"(0x0F0F0F0Fu), "r"(a), "r"(b));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// One row's output, D values spread over the threads: y[d] = o[d] * by.
-__device__ __forceinline__ void kv_store(const KvAttnArgs &a, int64_t at, float v) {
-  if (a.s_out)
-    static_cast<uint8_t *>(a.out)[at] = static_cast<uint8_t>(cvt_e4m3x2(v, 0.0f));
-  else
-    static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(v);
+// Four neighbouring values of a row's output.
+__device__ __forceinline__ void kv_store4(const KvAttnArgs &a, int64_t at, float4 v) {
+  if (a.s_out) {
+    *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(a.out) + at) =
+        pack4(cvt_e4m3x2(v.x, v.y), cvt_e4m3x2(v.z, v.w));
+  } else {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) = make_uint2(
+        *reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+  }
 }
 
 template <int D, int NT>
 struct KvRowsCfg {
   static constexpr int ROWS = 8 * NT;
-  static constexpr int STAGE = 4 * strip_bytes(D);
-  static constexpr int RING = kKvRowWarps * kKvStages * STAGE;
-  static constexpr int MERGE = kKvRowWarps * ROWS * (D + 2) * 4;  // laid over the ring
-  static constexpr int SMEM = (RING > MERGE ? RING : MERGE) + 128;
+  static constexpr int SLOT = 2 * strip_bytes(D);
+  static constexpr int RING = kKvSlots * SLOT;
+  static constexpr int MERGE = kKvRowWarps * ROWS * (D + 2) * 4;
+  static constexpr int SMEM = RING + MERGE;
+};
+
+// Barrier of the consumer warps alone.
+__device__ __forceinline__ void consumers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kKvRowWarps * 32) : "memory");
+}
+
+// One part of a block's range: units [k0, k1) of a (request, head, row tile).
+struct KvSegment {
+  KvRequest req;
+  int64_t begin;  // its first unit in the whole sequence
+  int64_t first;  // the first one of the part
+  int b, head, tile, tiles, chunks, k0, k1;
+  int strip0, strip1;  // the strips of [k0, k1) that hold tokens
+  int per_slot;        // strips of a ring slot: few of them are spread over the warps
+};
+
+// Walks a block's range segment by segment; the producer and the consumers
+// walk it alike.
+template <int ROWS>
+struct KvWalk {
+  const KvAttnArgs &a;
+  int64_t u, end, before;
+  int b;
+
+  // The next part with a chunk in it (a range may end in a segment's fixed cost).
+  __device__ bool next(KvSegment &s) {
+    do {
+      if (!step(s)) return false;
+    } while (s.k1 <= s.k0);
+    return true;
+  }
+
+  __device__ bool step(KvSegment &s) {
+    if (u >= end || b >= a.batch) return false;
+    int64_t units = kv_units<ROWS>(a, b, s.tiles, s.chunks);
+    while (u >= before + units && b + 1 < a.batch) {
+      before += units;
+      units = kv_units<ROWS>(a, ++b, s.tiles, s.chunks);
+    }
+    if (u >= before + units) return false;  // the lengths changed under the kernel
+    const int cost = s.chunks + kKvSegmentCost;
+    // head-major over (head, row tile); 32 bits but for absurd sizes
+    const int64_t seg = units <= INT32_MAX ? static_cast<int>(u - before) / cost
+                                           : (u - before) / cost;
+    s.req = kv_request(a, b);
+    s.b = b;
+    s.begin = before + seg * cost;
+    s.first = u;
+    s.k0 = max(static_cast<int>(u - s.begin) - kKvSegmentCost, 0);
+    s.k1 = static_cast<int>(min(end - s.begin, static_cast<int64_t>(cost))) - kKvSegmentCost;
+    s.head = static_cast<int>(units <= INT32_MAX ? static_cast<int>(seg) / s.tiles : seg / s.tiles);
+    s.tile = static_cast<int>(seg - static_cast<int64_t>(s.head) * s.tiles);
+    constexpr int per_chunk = kKvChunk / kStripTokens;
+    s.strip0 = s.k0 * per_chunk;
+    s.strip1 = max(s.strip0, min(s.k1 * per_chunk, (s.req.kv + kStripTokens - 1) / kStripTokens));
+    s.per_slot = s.strip1 - s.strip0 >= 2 * kKvRowWarps ? 2 : 1;
+    u = s.begin + s.k1 + kKvSegmentCost;
+    return true;
+  }
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kKvRowThreads, 3)
+__global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
     fp4_kv_rows_kernel(const KvAttnArgs a, uint64_t timeout_ns) {
   using C = KvRowsCfg<D, NT>;
   constexpr int ROWS = C::ROWS;
   constexpr int KB = D / 8;    // code bytes of a row that a thread holds (K), D/8 elements of V
   constexpr int TILES = D / 16;  // K steps of the first product, 16-row tiles of the second
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t full[kKvRowWarps][kKvStages];
+  __shared__ __align__(8) uint64_t full[kKvSlots], empty[kKvSlots];
+  __shared__ uint32_t present[kKvSlots];  // which strips of a slot exist
   __shared__ int abort_flag;
   __shared__ int64_t s_first[3];  // units before request b0; in all; b0
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int g = lane / 4, t = lane % 4;  // fragment coordinates
 
-  if (lane == 0) {
-    for (int s = 0; s < kKvStages; ++s) mbar_init(&full[warp][s], 1);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kKvSlots; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    abort_flag = 0;
     fence_mbar_init();
   }
-  if (threadIdx.x == 0) abort_flag = 0;
   pdl_launch_dependents();
   pdl_wait();
 
@@ -190,41 +279,86 @@ __global__ void __launch_bounds__(kKvRowThreads, 3)
   const int64_t all = s_first[1];
   const int64_t per = (all + gridDim.x - 1) / gridDim.x;
   const int64_t begin = per * blockIdx.x;
-  const int64_t end = min(begin + per, all);
-  if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  KvWalk<ROWS> walk{a, begin, min(begin + per, all), s_first[0], static_cast<int>(s_first[2])};
+  KvSegment seg;
+  uint32_t seq0 = 0;  // ring slots used by the segments before
 
-  uint8_t *ring = smem + warp * kKvStages * C::STAGE;
-  uint32_t phase = 0;  // bit per slot
+  if (warp == kKvRowWarps) {
+    // ------------------------------------------------------------ producer
+    const uint64_t policy = l2_policy_evict_first();
+    bool ok = true;
+    while (ok && walk.next(seg)) {
+      const int32_t *table = a.table + static_cast<int64_t>(seg.b) * a.width;
+      auto page_of = [&](int strip) {
+        return strip < seg.strip1 ? table[(strip * kStripTokens) >> a.cache.page_shift] : -1;
+      };
+      const int S = seg.per_slot;
+      int page = page_of(seg.strip0 + lane);
+      for (int base = seg.strip0; base < seg.strip1 && ok; base += 32) {
+        const int strip = base + lane;  // each lane has one of 32 strips
+        const bool there = page >= 0 && page < a.cache.pages;
+        const uint8_t *src =
+            a.cache.data +
+            (((static_cast<int64_t>(there ? page : 0) * a.cache.heads + seg.head)
+              << (a.cache.page_shift - 4)) +
+             (strip & ((1 << (a.cache.page_shift - 4)) - 1))) *
+                strip_bytes(D);
+        const uint32_t exist = __ballot_sync(0xFFFFFFFFu, there);
+        page = page_of(strip + 32);
+        const int slots = (min(32, seg.strip1 - base) + S - 1) / S;
+        for (int i = 0; i < slots; ++i) {
+          const uint32_t seq = seq0++;
+          const uint32_t slot = seq % kKvSlots;
+          if (!mbar_wait_polled_warp(&empty[slot], (seq / kKvSlots & 1u) ^ 1u, &abort_flag,
+                                      timeout_ns)) {
+            if (lane == 0) {
+              record_timeout(kSiteKvRows);
+              *const_cast<volatile int *>(&abort_flag) = 1;
+            }
+            ok = false;
+            --seq0;
+            break;
+          }
+          const uint32_t mask = exist >> (i * S) & (S == 2 ? 3u : 1u);
+          if (lane == 0) {
+            present[slot] = mask;
+            mbar_arrive_expect_tx(&full[slot], __popc(mask) * strip_bytes(D));
+          }
+          __syncwarp();
+          if (lane / S == i && there)
+            bulk_load_1d(smem + slot * C::SLOT + (lane % S) * strip_bytes(D), src, strip_bytes(D),
+                         &full[slot], policy);
+        }
+      }
+    }
+    if (!ok) {  // copies in flight land before the block may end
+      int zero = 0;
+      for (uint32_t k = seq0 > kKvSlots ? seq0 - kKvSlots : 0; k < seq0; ++k)
+        mbar_wait_polled_warp(&full[k % kKvSlots], k / kKvSlots & 1u, &zero, timeout_ns);
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int g = lane / 4, t = lane % 4;  // fragment coordinates
+  float *mo = reinterpret_cast<float *>(smem + C::RING);  // [warp][row][D]
+  float *ml = mo + kKvRowWarps * ROWS * D;                // [warp][row][2]
   const float c2 = a.scale * 1.4426950408889634f * __ldg(a.s_k);
   const float out_by = a.s_out ? __ldg(a.s_v) / __ldg(a.s_out) : __ldg(a.s_v);
   bool ok = true;
-
-  int b = static_cast<int>(s_first[2]);
-  int64_t before = s_first[0];
-  for (int64_t u = begin; u < end && b < a.batch;) {
-    // ---------------------------------------------- the segment that u lies in
-    int tiles, chunks;
-    int64_t units = kv_units<ROWS>(a, b, tiles, chunks);
-    while (u >= before + units && b + 1 < a.batch) {
-      before += units;
-      units = kv_units<ROWS>(a, ++b, tiles, chunks);
-    }
-    if (u >= before + units) break;  // the lengths changed under the kernel
-    const KvRequest req = kv_request(a, b);
-    const int64_t seg = (u - before) / chunks;  // head-major over (head, row tile)
-    const int64_t seg_begin = before + seg * chunks;
-    const int k0 = static_cast<int>(u - seg_begin);
-    const int k1 = static_cast<int>(min(end - seg_begin, static_cast<int64_t>(chunks)));
-    const int head = static_cast<int>(seg / tiles), tile = static_cast<int>(seg % tiles);
-    const int row0 = tile * ROWS;
+  if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  while (walk.next(seg)) {
+    const KvRequest req = seg.req;
+    const int head = seg.head;
+    const int row0 = seg.tile * ROWS;
     const int rows = min(ROWS, req.q_len * a.group - row0);
-    const int32_t *table = a.table + static_cast<int64_t>(b) * a.width;
 
     // Q of row 8n + g, this thread's elements, as FP16 of q 2^-e with 2^e the
     // row's magnitude (exact but for elements below 2^-24 of the largest)
     uint32_t qf[NT][TILES][2];
     float cq[NT][2];  // 2^e c2 of this thread's two columns (rows 8n + 2t, + 1)
-    int lim[NT][2];
+    int lim[NT][2];   // tokens that they see
+    int all_see = req.kv;  // tokens that every row of the tile sees
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int r = 8 * n + g;
@@ -266,237 +400,225 @@ __global__ void __launch_bounds__(kKvRowThreads, 3)
         const int ec = __shfl_sync(0xFFFFFFFFu, e, col * 4);
         cq[n][y] = c2 * __uint_as_float(static_cast<uint32_t>(127 + ec) << 23);
         const int rr = 8 * n + col;
-        lim[n][y] = rr < rows ? kv_limit(req, (row0 + rr) / a.group, a.causal) : 0;
+        // columns without a row (their q is 0) see what there is
+        lim[n][y] = rr < rows ? kv_limit(req, (row0 + rr) / a.group, a.causal) : req.kv;
+        all_see = min(all_see, lim[n][y]);
       }
     }
+    all_see = min(all_see, __shfl_xor_sync(0xFFFFFFFFu, all_see, 1));
+    all_see = min(all_see, __shfl_xor_sync(0xFFFFFFFFu, all_see, 2));
 
     float o[NT][TILES][4];
-    float m[NT][2], l[NT][2];
+    float neg_m[NT][2], l[NT][2];  // minus the running maximum (log2 units), the sums
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int x = 0; x < TILES; ++x)
 #pragma unroll
         for (int y = 0; y < 4; ++y) o[n][x][y] = 0.0f;
-      m[n][0] = m[n][1] = -INFINITY;
+      neg_m[n][0] = neg_m[n][1] = INFINITY;
       l[n][0] = l[n][1] = 0.0f;
     }
 
-    // -------------------------------------------------- this warp's strips
-    const int strip0 = k0 * (kKvChunk / kStripTokens);
-    const int strip1 = min(k1 * (kKvChunk / kStripTokens), (req.kv + kStripTokens - 1) / kStripTokens);
-    const int n_strips = max(strip1 - strip0, 0);
-    // strips of a step: few of them are spread over the warps
-    const int S = n_strips >= 4 * kKvRowWarps ? 4 : (n_strips >= 2 * kKvRowWarps ? 2 : 1);
-    const int steps = (n_strips + S * kKvRowWarps - 1) / (S * kKvRowWarps);
-    // lane l < S looks up the page of strip l of a step
-    auto page_of = [&](int step) -> int {
-      const int strip = strip0 + (step * kKvRowWarps + warp) * S + lane;
-      if (step >= steps || lane >= S || strip >= strip1) return -1;
-      return table[(strip * kStripTokens) >> a.cache.page_shift];
-    };
-    // starts the copies of a step's strips; returns which of them exist
-    auto fetch = [&](int step, int page) -> uint32_t {
-      const bool there = page >= 0 && page < a.cache.pages;
-      const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there);
-      const int slot = step % kKvStages;
-      if (lane == 0 && mask)
-        mbar_arrive_expect_tx(&full[warp][slot], __popc(mask) * strip_bytes(D));
-      __syncwarp();
-      if (there) {
-        const int strip = strip0 + (step * kKvRowWarps + warp) * S + lane;
-        const int in_page = strip & ((1 << (a.cache.page_shift - 4)) - 1);
-        const uint8_t *src =
-            a.cache.data +
-            (((static_cast<int64_t>(page) * a.cache.heads + head) << (a.cache.page_shift - 4)) +
-             in_page) *
-                strip_bytes(D);
-        bulk_load_1d(ring + slot * C::STAGE + lane * strip_bytes(D), src, strip_bytes(D),
-                     &full[warp][slot], l2_policy_evict_first());
-      }
-      return mask;
-    };
-    uint32_t masks[kKvStages];
-    int next_page = page_of(0);
+    // NS neighbouring strips of shared memory at once (the second one's
+    // arithmetic fills the first one's waits)
+    auto multiply = [&](auto ns, const uint8_t *strips, int tok0) {
+      constexpr int NS = decltype(ns)::value;
+      // ---------------------------------------------- S^T = K Q^T
+      float s[NS][NT][4];
 #pragma unroll
-    for (int s = 0; s < kKvStages; ++s) {
-      masks[s] = s < steps ? fetch(s, next_page) : 0;
-      next_page = page_of(s + 1);
-    }
-    for (int step = 0; step < steps && ok; ++step) {
-      const int slot = step % kKvStages;
-      uint32_t mask = masks[0];
+      for (int z = 0; z < NS; ++z) {
+        const uint8_t *strip = strips + z * strip_bytes(D);
 #pragma unroll
-      for (int s = 1; s < kKvStages; ++s)
-        if (slot == s) mask = masks[s];
-      if (mask) {
-        if (!mbar_wait_bounded_warp(&full[warp][slot], (phase >> slot) & 1u, &abort_flag,
-                                    timeout_ns)) {
-          if (lane == 0) {
-            record_timeout(kSiteKvRows);
-            *const_cast<volatile int *>(&abort_flag) = 1;
+        for (int n = 0; n < NT; ++n) s[z][n][0] = s[z][n][1] = s[z][n][2] = s[z][n][3] = 0.0f;
+        uint32_t kw[2][KB / 4];  // codes of rows g and g + 8
+        __half2 ks[2];           // their scales (two where a thread spans two groups)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = g + 8 * h;
+          uint32_t sc;
+          if constexpr (D == 128) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(strip + row * 64 + 16 * t);
+            kw[h][0] = w.x;
+            kw[h][1] = w.y;
+            kw[h][2] = w.z;
+            kw[h][3] = w.w;
+            sc = cvt_f16_e4m3x2(
+                *reinterpret_cast<const uint16_t *>(strip + strip_ks(D) + row * 8 + 2 * t));
+          } else {
+            const uint2 w = *reinterpret_cast<const uint2 *>(strip + row * 32 + 8 * t);
+            kw[h][0] = w.x;
+            kw[h][1] = w.y;
+            sc = cvt_f16_e4m3x2(strip[strip_ks(D) + row * 4 + t]);
           }
-          ok = false;
-          break;
+          ks[h] = *reinterpret_cast<const __half2 *>(&sc);
         }
-        phase ^= 1u << slot;
-      }
-      const int first = strip0 + (step * kKvRowWarps + warp) * S;
-#pragma unroll 1
-      for (int i = 0; i < S; ++i) {
-        if (!(mask >> i & 1u)) continue;
-        const uint8_t *strip = ring + slot * C::STAGE + i * strip_bytes(D);
-        const int tok0 = (first + i) * kStripTokens;
-        // ---------------------------------------------- S^T = K Q^T
-        float s[NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
-        {
-          uint32_t kw[2][KB / 4];  // codes of rows g and g + 8
-          uint32_t ks[2];          // their scales, FP16 (two where a thread spans two groups)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int row = g + 8 * h;
-            if constexpr (D == 128) {
-              const uint4 w = *reinterpret_cast<const uint4 *>(strip + row * 64 + 16 * t);
-              kw[h][0] = w.x;
-              kw[h][1] = w.y;
-              kw[h][2] = w.z;
-              kw[h][3] = w.w;
-              ks[h] = cvt_f16_e4m3x2(
-                  *reinterpret_cast<const uint16_t *>(strip + strip_ks(D) + row * 8 + 2 * t));
-            } else {
-              const uint2 w = *reinterpret_cast<const uint2 *>(strip + row * 32 + 8 * t);
-              kw[h][0] = w.x;
-              kw[h][1] = w.y;
-              ks[h] = cvt_f16_e4m3x2(strip[strip_ks(D) + row * 4 + t]);
-            }
-          }
-#pragma unroll
-          for (int x = 0; x < KB / 4; ++x) {
-            // scale of this word's 8 elements, in both halves
-            const uint32_t sel = (D == 128 && x >= 2) ? 0x3232u : 0x1010u;
-            const uint32_t s0 = __byte_perm(ks[0], 0, sel), s1 = __byte_perm(ks[1], 0, sel);
-            uint32_t h0[4], h1[4];
-            cvt_f16_e2m1x8(kw[0][x], h0);
-            cvt_f16_e2m1x8(kw[1][x], h1);
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              h0[y] = mul_f16x2(h0[y], s0);
-              h1[y] = mul_f16x2(h1[y], s1);
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma_f16(s[n], h0[0], h1[0], h0[1], h1[1], qf[n][2 * x][0], qf[n][2 * x][1]);
-              mma_f16(s[n], h0[2], h1[2], h0[3], h1[3], qf[n][2 * x + 1][0], qf[n][2 * x + 1][1]);
-            }
-          }
-        }
-        // ---------------------------------------------- softmax of the 16 tokens
-        uint32_t p[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int x = 0; x < KB / 4; ++x) {
+          // scale of this word's 8 elements, in both halves
+          const bool second = D == 128 && x >= 2;
+          const __half2 s0 = second ? __high2half2(ks[0]) : __low2half2(ks[0]);
+          const __half2 s1 = second ? __high2half2(ks[1]) : __low2half2(ks[1]);
+          uint32_t h0[4], h1[4];
+          cvt_f16_e2m1x8(kw[0][x], h0);
+          cvt_f16_e2m1x8(kw[1][x], h1);
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            const int tok = tok0 + g + 8 * (y >> 1);
-            s[n][y] = tok < lim[n][y & 1] ? s[n][y] * cq[n][y & 1] : -INFINITY;
+            h0[y] = scaled(h0[y], s0);
+            h1[y] = scaled(h1[y], s1);
           }
-          const bool over = s[n][0] > m[n][0] + kKvSlack || s[n][2] > m[n][0] + kKvSlack ||
-                            s[n][1] > m[n][1] + kKvSlack || s[n][3] > m[n][1] + kKvSlack;
-          if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              float top = fmaxf(s[n][y], s[n][y + 2]);
-#pragma unroll
-              for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-              const float now = fmaxf(m[n][y], top);
-              const float by = now == -INFINITY ? 1.0f : ex2_approx(m[n][y] - now);
-              m[n][y] = now;
-              l[n][y] *= by;
-#pragma unroll
-              for (int x = 0; x < TILES; ++x) {
-                o[n][x][y] *= by;
-                o[n][x][y + 2] *= by;
-              }
-            }
+          for (int n = 0; n < NT; ++n) {
+            mma_f16(s[z][n], h0[0], h1[0], h0[1], h1[1], qf[n][2 * x][0], qf[n][2 * x][1]);
+            mma_f16(s[z][n], h0[2], h1[2], h0[3], h1[3], qf[n][2 * x + 1][0], qf[n][2 * x + 1][1]);
           }
-          const float m0 = m[n][0] == -INFINITY ? 0.0f : m[n][0];
-          const float m1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
-          const float p0 = ex2_approx(s[n][0] - m0), p1 = ex2_approx(s[n][1] - m1);
-          const float p2 = ex2_approx(s[n][2] - m0), p3 = ex2_approx(s[n][3] - m1);
-          l[n][0] += p0 + p2;
-          l[n][1] += p1 + p3;
-          // P is rounded to FP16 (2^-11 of each weight) for the second product
-          p[n][0] = transpose_8x8(pack_f16(p0, p1));
-          p[n][1] = transpose_8x8(pack_f16(p2, p3));
         }
-        // ---------------------------------------------- O^T += V^T P^T
-        {
-          const uint8_t *vc = strip + strip_v(D), *vs = strip + strip_vs(D);
-          uint32_t vw[4][KB / 8];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9: D/8 elements
-          uint32_t sc[4];
+      }
+      // ---------------------------------------------- softmax
+      const bool edge = tok0 + NS * kStripTokens > all_see;
+      uint32_t p[NS][NT][2];
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const int row = 2 * t + (h & 1) + 8 * (h >> 1);
-            if constexpr (D == 128) {
-              const uint2 w = *reinterpret_cast<const uint2 *>(vc + row * 64 + 8 * g);
-              vw[h][0] = w.x;
-              vw[h][1] = w.y;
-              sc[h] = vs[row * 8 + g];
-            } else {
-              vw[h][0] = *reinterpret_cast<const uint32_t *>(vc + row * 32 + 4 * g);
-              sc[h] = vs[row * 4 + g / 2];
-            }
-            // places past the last token hold anything, a NaN scale too
-            if (tok0 + row >= req.kv) sc[h] = 0;
-          }
-          const uint32_t s0 = cvt_f16_e4m3x2(sc[0] | sc[1] << 8);
-          const uint32_t s1 = cvt_f16_e4m3x2(sc[2] | sc[3] << 8);
+      for (int n = 0; n < NT; ++n) {
+        float e[NS][4];  // log2 of the weights
+        auto exponents = [&] {
 #pragma unroll
-          for (int x = 0; x < KB / 8; ++x) {
-            // bytes of (token, token + 1) for even and for odd elements
-            const uint32_t e0 = (vw[0][x] & 0x0F0F0F0Fu) | (vw[1][x] << 4 & 0xF0F0F0F0u);
-            const uint32_t d0 = (vw[0][x] >> 4 & 0x0F0F0F0Fu) | (vw[1][x] & 0xF0F0F0F0u);
-            const uint32_t e1 = (vw[2][x] & 0x0F0F0F0Fu) | (vw[3][x] << 4 & 0xF0F0F0F0u);
-            const uint32_t d1 = (vw[2][x] >> 4 & 0x0F0F0F0Fu) | (vw[3][x] & 0xF0F0F0F0u);
-            uint32_t he0[4], hd0[4], he1[4], hd1[4];
-            cvt_f16_e2m1x8(e0, he0);
-            cvt_f16_e2m1x8(d0, hd0);
-            cvt_f16_e2m1x8(e1, he1);
-            cvt_f16_e2m1x8(d1, hd1);
+          for (int z = 0; z < NS; ++z)
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              const uint32_t a0 = mul_f16x2(he0[y], s0), a1 = mul_f16x2(hd0[y], s0);
-              const uint32_t a2 = mul_f16x2(he1[y], s1), a3 = mul_f16x2(hd1[y], s1);
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-                mma_f16(o[n][4 * x + y], a0, a1, a2, a3, p[n][0], p[n][1]);
+              e[z][y] = fmaf(s[z][n][y], cq[n][y & 1], neg_m[n][y & 1]);
+              if (edge && tok0 + z * kStripTokens + g + 8 * (y >> 1) >= lim[n][y & 1])
+                e[z][y] = -INFINITY;
             }
+        };
+        exponents();
+        float top[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          top[y] = fmaxf(e[0][y], e[0][y + 2]);
+#pragma unroll
+          for (int z = 1; z < NS; ++z) top[y] = fmaxf(top[y], fmaxf(e[z][y], e[z][y + 2]));
+        }
+        if (__any_sync(0xFFFFFFFFu, fmaxf(top[0], top[1]) > kKvSlack)) {
+          // move the maxima (at first from -inf) to the largest scores
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float old = neg_m[n][y];
+            neg_m[n][y] = 0.0f;  // the scores themselves
+            top[y] = -old;
+          }
+          exponents();
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const float old = -top[y];
+            float now = top[y];
+#pragma unroll
+            for (int z = 0; z < NS; ++z) now = fmaxf(now, fmaxf(e[z][y], e[z][y + 2]));
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1)
+              now = fmaxf(now, __shfl_xor_sync(0xFFFFFFFFu, now, d));
+            // nothing seen yet: sums and maximum stay as they are
+            const float by = now == -INFINITY ? 1.0f : ex2_approx(-now - old);
+            neg_m[n][y] = now == -INFINITY ? INFINITY : -now;
+            l[n][y] *= by;
+#pragma unroll
+            for (int x = 0; x < TILES; ++x) {
+              o[n][x][y] *= by;
+              o[n][x][y + 2] *= by;
+            }
+          }
+          exponents();
+        }
+#pragma unroll
+        for (int z = 0; z < NS; ++z) {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) e[z][y] = ex2_approx(e[z][y]);
+          l[n][0] += e[z][0] + e[z][2];
+          l[n][1] += e[z][1] + e[z][3];
+          // P is rounded to FP16 (2^-11 of each weight) for the second product
+          p[z][n][0] = transpose_8x8(pack_f16(e[z][0], e[z][1]));
+          p[z][n][1] = transpose_8x8(pack_f16(e[z][2], e[z][3]));
+        }
+      }
+      // ---------------------------------------------- O^T += V^T P^T
+#pragma unroll
+      for (int z = 0; z < NS; ++z) {
+        const uint8_t *strip = strips + z * strip_bytes(D);
+        const uint8_t *vc = strip + strip_v(D), *vs = strip + strip_vs(D);
+        uint32_t vw[4][KB / 8];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9: D/8 elements
+        uint32_t sc[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const int row = 2 * t + (h & 1) + 8 * (h >> 1);
+          if constexpr (D == 128) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(vc + row * 64 + 8 * g);
+            vw[h][0] = w.x;
+            vw[h][1] = w.y;
+            sc[h] = vs[row * 8 + g];
+          } else {
+            vw[h][0] = *reinterpret_cast<const uint32_t *>(vc + row * 32 + 4 * g);
+            sc[h] = vs[row * 4 + g / 2];
+          }
+        }
+        if (tok0 + (z + 1) * kStripTokens > req.kv) {
+          // places past the last token hold anything, a NaN scale too
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            if (tok0 + z * kStripTokens + 2 * t + (h & 1) + 8 * (h >> 1) >= req.kv) sc[h] = 0;
+        }
+        const uint32_t s0 = cvt_f16_e4m3x2(__byte_perm(sc[0], sc[1], 0x0040));
+        const uint32_t s1 = cvt_f16_e4m3x2(__byte_perm(sc[2], sc[3], 0x0040));
+#pragma unroll
+        for (int x = 0; x < KB / 8; ++x) {
+          // bytes of (token, token + 1) for even and for odd elements
+          uint32_t he0[4], hd0[4], he1[4], hd1[4];
+          cvt_f16_e2m1x8(low_high_nibbles(vw[0][x], vw[1][x] << 4), he0);
+          cvt_f16_e2m1x8(low_high_nibbles(vw[0][x] >> 4, vw[1][x]), hd0);
+          cvt_f16_e2m1x8(low_high_nibbles(vw[2][x], vw[3][x] << 4), he1);
+          cvt_f16_e2m1x8(low_high_nibbles(vw[2][x] >> 4, vw[3][x]), hd1);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t a0 = mul_f16x2(he0[y], s0), a1 = mul_f16x2(hd0[y], s0);
+            const uint32_t a2 = mul_f16x2(he1[y], s1), a3 = mul_f16x2(hd1[y], s1);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma_f16(o[n][4 * x + y], a0, a1, a2, a3, p[z][n][0], p[z][n][1]);
           }
         }
       }
-      __syncwarp();  // the slot is read: it may be filled again
-      const uint32_t fresh = step + kKvStages < steps ? fetch(step + kKvStages, next_page) : 0;
-#pragma unroll
-      for (int s = 0; s < kKvStages; ++s)
-        if (slot == s) masks[s] = fresh;
-      next_page = page_of(step + kKvStages + 1);
-    }
-    if (!ok) {  // copies in flight land before the block goes on to leave
-      int zero = 0;
-      for (int s = 0; s < kKvStages; ++s) {
-        bool pending = false;
-#pragma unroll
-        for (int z = 0; z < kKvStages; ++z)
-          if (z == s) pending = masks[z] != 0;
-        if (pending) mbar_wait_bounded_warp(&full[warp][s], (phase >> s) & 1u, &zero, timeout_ns);
+    };
+
+    const int S = seg.per_slot;
+    const int slots = (seg.strip1 - seg.strip0 + S - 1) / S;
+    for (int i = warp; i < slots && ok; i += kKvRowWarps) {
+      const uint32_t seq = seq0 + i;
+      const uint32_t slot = seq % kKvSlots;
+      if (!mbar_wait_polled_warp(&full[slot], seq / kKvSlots & 1u, &abort_flag, timeout_ns)) {
+        if (lane == 0) {
+          record_timeout(kSiteKvRows);
+          *const_cast<volatile int *>(&abort_flag) = 1;
+        }
+        ok = false;
+        break;
       }
+      const uint32_t mask = present[slot];
+      const uint8_t *at = smem + slot * C::SLOT;
+      const int tok0 = (seg.strip0 + i * S) * kStripTokens;
+      // two strips at once, but for 16 rows of 128, whose sums take the registers
+      if (NT * D <= 128 && mask == 3u) {
+        multiply(std::integral_constant<int, 2>{}, at, tok0);
+      } else {
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x)
+          if (mask >> x & 1u)
+            multiply(std::integral_constant<int, 1>{}, at + x * strip_bytes(D),
+                     tok0 + x * kStripTokens);
+      }
+      __syncwarp();  // the slot is read: it may be filled again
+      if (lane == 0) mbar_arrive(&empty[slot]);
     }
+    seq0 += slots;
 
     // ---------------------------------------------- the four warps' sums
-    float *mo = reinterpret_cast<float *>(smem);  // [warp][row][D]
-    float *ml = mo + kKvRowWarps * ROWS * D;      // [warp][row][2]
-    __syncthreads();  // every warp is done with its ring
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -505,7 +627,7 @@ __global__ void __launch_bounds__(kKvRowThreads, 3)
         for (int d = 4; d < 32; d <<= 1) l[n][y] += __shfl_xor_sync(0xFFFFFFFFu, l[n][y], d);
         const int row = warp * ROWS + 8 * n + 2 * t + y;
         if (g == 0) {
-          ml[2 * row] = m[n][y];
+          ml[2 * row] = -neg_m[n][y];
           ml[2 * row + 1] = l[n][y];
         }
 #pragma unroll
@@ -514,61 +636,74 @@ __global__ void __launch_bounds__(kKvRowThreads, 3)
               make_float2(o[n][x][y], o[n][x][y + 2]);
       }
     }
-    __syncthreads();
-    const bool whole = k0 == 0 && k1 == chunks;
+    consumers_sync();
+    const bool whole = seg.k0 == 0 && seg.k1 == seg.chunks;
     // partial sums: slot 2c for the segment that block c's range starts in,
     // 2c + 1 for one that starts inside the range
-    const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (u == begin ? 0 : 1);
+    const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (seg.first == begin ? 0 : 1);
     float *pml = a.part + 2 * static_cast<int64_t>(gridDim.x) * ROWS * D;
-    for (int x = threadIdx.x; x < rows * D; x += kKvRowThreads) {
-      const int row = x / D, d = x % D;
+    for (int x = threadIdx.x; x < rows * (D / 4); x += kKvRowWarps * 32) {
+      const int row = x / (D / 4), d = 4 * (x % (D / 4));
       float top = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kKvRowWarps; ++w) top = fmaxf(top, ml[2 * (w * ROWS + row)]);
       const float base = top == -INFINITY ? 0.0f : top;
-      float sum = 0.0f, val = 0.0f;
+      float sum = 0.0f;
+      float4 val = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int w = 0; w < kKvRowWarps; ++w) {
         const float by = ex2_approx(ml[2 * (w * ROWS + row)] - base);
+        const float4 v = *reinterpret_cast<const float4 *>(mo + (w * ROWS + row) * D + d);
         sum += by * ml[2 * (w * ROWS + row) + 1];
-        val += by * mo[(w * ROWS + row) * D + d];
+        val.x += by * v.x;
+        val.y += by * v.y;
+        val.z += by * v.z;
+        val.w += by * v.w;
       }
       if (whole) {
         const int i = (row0 + row) / a.group;
         const int64_t at = (static_cast<int64_t>(req.q0 + i) * a.cache.heads + head) * a.group +
                            (row0 + row) % a.group;
-        kv_store(a, at * D + d, sum != 0.0f ? val / sum * out_by : 0.0f);
+        const float by = sum != 0.0f ? out_by / sum : 0.0f;
+        kv_store4(a, at * D + d, make_float4(val.x * by, val.y * by, val.z * by, val.w * by));
         if (a.lse && d == 0) a.lse[at] = (top + log2f(sum)) * 0.6931471805599453f;
       } else {
-        a.part[(piece * ROWS + row) * D + d] = val;
+        *reinterpret_cast<float4 *>(a.part + (piece * ROWS + row) * D + d) = val;
         if (d == 0) {
           pml[2 * (piece * ROWS + row)] = top;
           pml[2 * (piece * ROWS + row) + 1] = sum;
         }
       }
     }
-    fence_async_shared();  // the sums above lie where copies will land next
-    __syncthreads();
+    consumers_sync();  // the sums are read: they may be overwritten
     // The first boundary inside a segment is where it is merged: block c,
     // whose range starts inside the segment, if block c - 1's did not.
-    if (!whole && u == begin && k0 > 0 && threadIdx.x == 0) {
-      const int64_t first_block = seg_begin / per;
+    if (!whole && seg.first == begin && seg.k0 > 0 && threadIdx.x == 0) {
+      const int64_t first_block = (seg.begin + kKvSegmentCost) / per;
       if (first_block == static_cast<int64_t>(blockIdx.x) - 1) {
-        const int64_t last_block = (seg_begin + chunks - 1) / per;
-        const int head_piece = seg_begin == first_block * per ? 0 : 1;
+        const int64_t last_block = (seg.begin + kKvSegmentCost + seg.chunks - 1) / per;
+        const int head_piece = seg.begin <= first_block * per ? 0 : 1;
         a.meta[blockIdx.x] =
-            make_int4(b, head, tile * 2 + head_piece, static_cast<int>(last_block));
+            make_int4(seg.b, head, seg.tile * 2 + head_piece, static_cast<int>(last_block));
       }
     }
-    u = seg_begin + k1;
   }
 }
 
 // Adds the partial sums of a segment that several blocks worked on, in block
-// order.  Block c merges the segment whose first block is c - 1.
+// order.  Block c merges the segment whose first block is c - 1.  All latency:
+// a thread owns 4 of a row's D values and every SPLIT-th piece, whose
+// loads do not depend on one another, and the shares meet in shared memory.
+constexpr int kKvMergeThreads = 512;
+
 template <int D, int NT>
-__global__ void __launch_bounds__(D) fp4_kv_merge_kernel(const KvAttnArgs a, int blocks) {
+__global__ void __launch_bounds__(kKvMergeThreads)
+    fp4_kv_merge_kernel(const KvAttnArgs a, int blocks) {
   constexpr int ROWS = 8 * NT;
+  constexpr int LANES = D / 4;
+  constexpr int SPLIT = kKvMergeThreads / (ROWS * LANES);
+  __shared__ float4 s_val[SPLIT][ROWS][LANES];
+  __shared__ float s_sum[SPLIT][ROWS];
   pdl_launch_dependents();
   pdl_wait();
   const int4 w = a.meta[blockIdx.x + 1];
@@ -577,26 +712,51 @@ __global__ void __launch_bounds__(D) fp4_kv_merge_kernel(const KvAttnArgs a, int
   const int head = w.y, row0 = (w.z >> 1) * ROWS;
   const KvRequest req = kv_request(a, w.x);
   const int rows = min(ROWS, req.q_len * a.group - row0);
+  const int lane = threadIdx.x % LANES, row = threadIdx.x / LANES % ROWS;
+  const int share = threadIdx.x / (LANES * ROWS);
   const float *pml = a.part + 2 * static_cast<int64_t>(blocks) * ROWS * D;
-  const float out_by = a.s_out ? __ldg(a.s_v) / __ldg(a.s_out) : __ldg(a.s_v);
-  for (int row = 0; row < rows; ++row) {
-    float top = -INFINITY, sum = 0.0f, val = 0.0f;
-    for (int c = first; c <= last; ++c) {
-      const int64_t at = (2 * static_cast<int64_t>(c) + (c == first ? (w.z & 1) : 0)) * ROWS + row;
-      const float m = pml[2 * at], l = pml[2 * at + 1], v = a.part[at * D + threadIdx.x];
-      const float now = fmaxf(top, m);
-      const float base = now == -INFINITY ? 0.0f : now;
-      const float x = ex2_approx(top - base), y = ex2_approx(m - base);
-      sum = sum * x + l * y;
-      val = val * x + v * y;
-      top = now;
-    }
-    const int i = (row0 + row) / a.group;
-    const int64_t at = (static_cast<int64_t>(req.q0 + i) * a.cache.heads + head) * a.group +
-                       (row0 + row) % a.group;
-    kv_store(a, at * D + threadIdx.x, sum != 0.0f ? val / sum * out_by : 0.0f);
-    if (a.lse && threadIdx.x == 0) a.lse[at] = (top + log2f(sum)) * 0.6931471805599453f;
+  // piece of block c: the first block's may be its second one
+  auto piece = [&](int c) {
+    return (2 * static_cast<int64_t>(c) + (c == first ? (w.z & 1) : 0)) * ROWS + row;
+  };
+  float top = -INFINITY;
+#pragma unroll 8
+  for (int c = first; c <= last; ++c) top = fmaxf(top, pml[2 * piece(c)]);
+  const float base = top == -INFINITY ? 0.0f : top;
+  float sum = 0.0f;
+  float4 val = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int c = first + share; c <= last; c += SPLIT) {
+    const int64_t at = piece(c);
+    const float by = ex2_approx(pml[2 * at] - base);
+    const float4 v = *reinterpret_cast<const float4 *>(a.part + at * D + 4 * lane);
+    sum += by * pml[2 * at + 1];
+    val.x += by * v.x;
+    val.y += by * v.y;
+    val.z += by * v.z;
+    val.w += by * v.w;
   }
+  s_val[share][row][lane] = val;
+  if (lane == 0) s_sum[share][row] = sum;
+  __syncthreads();
+  if (share != 0 || row >= rows) return;
+#pragma unroll
+  for (int x = 1; x < SPLIT; ++x) {
+    const float4 v = s_val[x][row][lane];
+    sum += s_sum[x][row];
+    val.x += v.x;
+    val.y += v.y;
+    val.z += v.z;
+    val.w += v.w;
+  }
+  const float out_by = a.s_out ? __ldg(a.s_v) / __ldg(a.s_out) : __ldg(a.s_v);
+  const float by = sum != 0.0f ? out_by / sum : 0.0f;
+  const int i = (row0 + row) / a.group;
+  const int64_t at = (static_cast<int64_t>(req.q0 + i) * a.cache.heads + head) * a.group +
+                     (row0 + row) % a.group;
+  kv_store4(a, at * D + 4 * lane,
+            make_float4(val.x * by, val.y * by, val.z * by, val.w * by));
+  if (a.lse && lane == 0) a.lse[at] = (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 }  // namespace fp8ws

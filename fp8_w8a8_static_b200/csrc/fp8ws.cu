@@ -988,13 +988,16 @@ int launch_kv_rows(DeviceInfo *d, KvAttnArgs a, cudaStream_t st) {
                : FP8WS_ERR_CUDA;
   });
   if (rc) return rc;
-  const int blocks = 3 * d->sms < kKvMaxBlocks ? 3 * d->sms : kKvMaxBlocks;
+  const int want = kv_blocks_per_sm(NT) * d->sms;
+  const int blocks = want < kKvMaxBlocks ? want : kKvMaxBlocks;
   if (launch_ex(kern, dim3(blocks), dim3(kKvRowThreads), C::SMEM, st, 1, a, kWaitLimitNs) !=
       cudaSuccess)
     return FP8WS_ERR_CUDA;
   log_launch(kKindKvAttention, a.q, a.cache.data, a.out);
-  if (launch_ex(fp4_kv_merge_kernel<D, NT>, dim3(blocks - 1), dim3(D), 0, st, 1, a, blocks) !=
-      cudaSuccess)
+  // a segment of one chunk lies in one range
+  if ((a.width << a.cache.page_shift) <= kKvChunk) return launch_status();
+  if (launch_ex(fp4_kv_merge_kernel<D, NT>, dim3(blocks - 1),
+                dim3(kKvMergeThreads), 0, st, 1, a, blocks) != cudaSuccess)
     return FP8WS_ERR_CUDA;
   log_launch(kKindKvAttention, a.part, nullptr, a.out);
   return launch_status();
