@@ -28,6 +28,7 @@ enum WaitSite : int {
   kSiteStagedEmpty = 8,  // staged quantizer: a ring slot that was not released
   kSiteKvRows = 9,       // attention over the 4-bit cache, few rows: strips that did not arrive
   kSiteEpiResidual = 10, // Linear with a fused epilogue: a residual box that did not arrive
+  kSiteKvTiles = 11,     // attention over the 4-bit cache, many rows: any of its waits
 };
 
 __device__ __forceinline__ void record_timeout(int site) {

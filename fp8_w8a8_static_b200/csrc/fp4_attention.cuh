@@ -64,6 +64,7 @@ struct KvAttnArgs {
   const float *s_v;
   float scale;
   int causal;
+  int few_rows;  // requests of more rows (tokens x group) are fp4_kv_tiles_kernel's
   const float *s_out;  // null: BF16 output
   void *out;
   float *lse;  // may be null
@@ -100,7 +101,8 @@ constexpr int kKvSegmentCost = 2;
 template <int ROWS>
 __device__ __forceinline__ int64_t kv_units(const KvAttnArgs &a, int b, int &tiles, int &chunks) {
   const KvRequest r = kv_request(a, b);
-  tiles = static_cast<int>((static_cast<int64_t>(r.q_len) * a.group + ROWS - 1) / ROWS);
+  const int rows = r.q_len * a.group;
+  tiles = rows <= a.few_rows ? (rows + ROWS - 1) / ROWS : 0;
   chunks = max(1, (r.kv + kKvChunk - 1) / kKvChunk);
   return static_cast<int64_t>(tiles) * a.cache.heads * (chunks + kKvSegmentCost);
 }

@@ -1,0 +1,580 @@
+// Attention over the 4-bit paged K/V cache for many query rows (prompts,
+// cross-attention), on the tensor cores of sm_100a (tcgen05).
+//
+// The operation, the cache and the row packing are those of fp4_attention.cuh.
+// A block takes 256 rows (two 128-row tiles) of one request and K/V head and
+// walks the tokens that any of them sees, 128 at a time:
+//   warp 0        copies strips into a two-slot ring (bulk copies, one a strip)
+//   warps 12..15  turn codes into FP16 once for both row tiles: K and V as
+//                 [token][64 elements] 128-byte-swizzled atoms.  K is read
+//                 K-major, V MN-major (its inner index, the token, is the row),
+//                 so both are written the same way and nothing is transposed.
+//   warp 1        issues the MMAs: S_t = Q_t K^T (M = 128, N = 128) into TMEM,
+//                 O_t += P_t V with P_t read from TMEM
+//   warps 4..11   softmax: four warps a row tile, a thread a row, so the maximum
+//                 and the sum need no exchange.  P (FP16) takes the place of S.
+// The two row tiles alternate: one's products run while the other's weights are
+// computed.  A row's maximum is moved, and its sums in TMEM scaled, only when a
+// score exceeds it by 2^10 (FP16 weights have that room).
+// Bound: 128 x 128 scores are 1024 cycles of the tensor pipe (D = 128: two
+// products of 512) and 1024 of the special function unit (one exponential
+// each, 16 a cycle), side by side; the codes' conversion is 256 cycles of the
+// conversion unit for 256 rows.
+#pragma once
+
+#include "common.cuh"
+#include "fp4_attention.cuh"
+
+namespace fp8ws {
+
+constexpr int kKvTileRows = 256;
+constexpr int kKvTileTokens = 128;
+constexpr int kKvTileStrips = kKvTileTokens / kStripTokens;
+constexpr int kKvTileThreads = 512;
+constexpr int kKvMasks = 8;  // tiles whose missing strips are remembered
+
+template <int D>
+struct KvTilesCfg {
+  static constexpr int ATOMS = D / 64;                 // 64-element atoms of a row
+  static constexpr int ATOM = 128 * 128;               // 128 rows of 128 bytes
+  static constexpr int TILE = ATOMS * ATOM;            // Q, K or V of 128 rows, FP16
+  static constexpr int RAW = kKvTileStrips * strip_bytes(D);
+  static constexpr int RAW_PAD = (RAW + 1023) / 1024 * 1024;
+  // two tiles of Q, one of K, two of V, two of raw strips
+  static constexpr int SMEM = 5 * TILE + 2 * RAW_PAD + 1024;
+  static constexpr int O_COL = 256;  // TMEM columns: S/P of both tiles, then O of both
+  static_assert(SMEM <= 232448, "shared memory");
+};
+
+// kind::f16 descriptor: FP16 A and B, fp32 D; B K-major or MN-major.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+  return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// MN-major operand in 128-byte-swizzled atoms of 64 elements (128 bytes) by 8
+// inner rows: 8-row groups 1024 bytes apart (stride), 64-element blocks `block`
+// bytes apart (leading).
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t block) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((block >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+__device__ __forceinline__ void umma_f16_ss(uint32_t tmem_d, uint64_t desc_a, uint64_t desc_b,
+                                            uint32_t idesc, uint32_t accumulate) {
+  uint32_t z = 0;  // no output lane disabled
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}" ::"r"(
+          tmem_d),
+      "l"(desc_a), "l"(desc_b), "r"(idesc), "r"(accumulate), "r"(z));
+}
+
+// A from TMEM: lane = row, a column holds two neighbouring elements.
+__device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t desc_b,
+                                            uint32_t idesc, uint32_t accumulate) {
+  uint32_t z = 0;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n\t}" ::"r"(
+          tmem_d),
+      "r"(tmem_a), "l"(desc_b), "r"(idesc), "r"(accumulate), "r"(z));
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// 256-row blocks of request b over all heads, 0 for a request whose rows the
+// other kernel takes.
+__device__ __forceinline__ int64_t kv_tile_items(const KvAttnArgs &a, int b) {
+  const KvRequest r = kv_request(a, b);
+  const int64_t rows = static_cast<int64_t>(r.q_len) * a.group;
+  if (rows <= a.few_rows) return 0;
+  return (rows + kKvTileRows - 1) / kKvTileRows * a.cache.heads;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kKvTileThreads, 1)
+    fp4_kv_tiles_kernel(const KvAttnArgs a, uint64_t timeout_ns) {
+  using C = KvTilesCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t *sQ = smem;                // [2] tiles
+  uint8_t *sK = smem + 2 * C::TILE;
+  uint8_t *sV = sK + C::TILE;        // [2]
+  uint8_t *sRaw = sV + 2 * C::TILE;  // [2]
+  __shared__ __align__(8) uint64_t raw_full[2], raw_empty[2], k_full, k_empty, v_full[2],
+      v_empty[2], s_full[2], p_full[2], pv_done[2], drain;
+  __shared__ uint32_t missing[kKvMasks];  // strips that the cache lacks, a bit each
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  __shared__ int s_item[2];  // request (-1: none), block and head within it
+  volatile int *abort_flag = &abort_word;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], 4);
+      mbar_init(&v_full[s], 4);
+      mbar_init(&v_empty[s], 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 4);
+      mbar_init(&pv_done[s], 1);
+    }
+    mbar_init(&k_full, 4);
+    mbar_init(&k_empty, 1);
+    mbar_init(&drain, 1);
+    abort_word = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+  if (warp == 0) {  // this block's request
+    int64_t before = 0;
+    int found = -1, local = 0;
+    for (int b0 = 0; b0 < a.batch && found < 0; b0 += 32) {
+      const int b = b0 + lane;
+      const int64_t mine = b < a.batch ? kv_tile_items(a, b) : 0;
+      int64_t n = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t m = __shfl_up_sync(0xFFFFFFFFu, n, d);
+        if (lane >= d) n += m;
+      }
+      const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + n > blockIdx.x);
+      if (past) {
+        const int src = __ffs(past) - 1;
+        found = b0 + src;
+        local = static_cast<int>(blockIdx.x -
+                                 (before + __shfl_sync(0xFFFFFFFFu, n - mine, src)));
+      }
+      before += __shfl_sync(0xFFFFFFFFu, n, 31);
+    }
+    if (lane == 0) {
+      s_item[0] = found;
+      s_item[1] = local;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int b = s_item[0];
+  if (b < 0) {  // more blocks than work
+    __syncthreads();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+    return;
+  }
+  const KvRequest req = kv_request(a, b);
+  const int total_rows = req.q_len * a.group;
+  const int blocks = (total_rows + kKvTileRows - 1) / kKvTileRows;
+  const int head = s_item[1] % a.cache.heads;
+  // the last rows, which see the most tokens, come first
+  const int row0 = (blocks - 1 - s_item[1] / a.cache.heads) * kKvTileRows;
+  const int rows = min(kKvTileRows, total_rows - row0);
+  const int row_tiles = rows > 128 ? 2 : 1;
+  // tokens that some row of the block sees, and that all of them see
+  const int most = kv_limit(req, (row0 + rows - 1) / a.group, a.causal);
+  const int tiles = (most + kKvTileTokens - 1) / kKvTileTokens;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const int32_t *table = a.table + static_cast<int64_t>(b) * a.width;
+    const int strips = (most + kStripTokens - 1) / kStripTokens;
+    auto page_of = [&](int strip) {
+      return lane < kKvTileStrips && strip < strips
+                 ? table[(strip * kStripTokens) >> a.cache.page_shift]
+                 : -1;
+    };
+    int page = page_of(lane);
+    int j = 0;
+    for (; j < tiles; ++j) {
+      const int slot = j & 1;
+      if (!mbar_wait_polled_warp(&raw_empty[slot], (j >> 1 & 1) ^ 1, abort_flag, timeout_ns)) {
+        if (lane == 0) {
+          record_timeout(kSiteKvTiles);
+          *abort_flag = 1;
+        }
+        break;
+      }
+      const int strip = j * kKvTileStrips + lane;
+      const bool there = page >= 0 && page < a.cache.pages;
+      const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there);
+      if (lane == 0) {
+        missing[j % kKvMasks] = ~mask & ((1u << kKvTileStrips) - 1);
+        mbar_arrive_expect_tx(&raw_full[slot], __popc(mask) * strip_bytes(D));
+      }
+      __syncwarp();
+      if (there) {
+        const int64_t at = ((static_cast<int64_t>(page) * a.cache.heads + head)
+                            << (a.cache.page_shift - 4)) +
+                           (strip & ((1 << (a.cache.page_shift - 4)) - 1));
+        bulk_load_1d(sRaw + slot * C::RAW_PAD + lane * strip_bytes(D),
+                     a.cache.data + at * strip_bytes(D), strip_bytes(D), &raw_full[slot],
+                     l2_policy_evict_normal());
+      }
+      page = page_of(strip + kKvTileStrips);
+    }
+    if (j < tiles) {  // copies in flight land before the block may end
+      int zero = 0;
+      for (int k = max(j - 2, 0); k < j; ++k)
+        mbar_wait_polled_warp(&raw_full[k & 1], k >> 1 & 1, &zero, timeout_ns);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issue
+    asm volatile("bar.sync 1, 288;" ::: "memory");  // Q is there
+    if (lane == 0 && tiles > 0) {
+      constexpr uint32_t idesc_s = idesc_f16_f32(128, kKvTileTokens, false);
+      constexpr uint32_t idesc_o = idesc_f16_f32(128, D, true);
+      // every barrier below completes once a tile
+      auto wait = [&](uint64_t *bar, int n) -> bool {
+        if (mbar_wait_bounded(bar, n & 1, abort_flag, timeout_ns)) {
+          tc_fence_after();
+          return true;
+        }
+        record_timeout(kSiteKvTiles);
+        *abort_flag = 1;
+        return false;
+      };
+      auto scores = [&](int t) {  // S_t = Q_t K^T
+        const uint32_t q = smem_u32(sQ + t * C::TILE), k = smem_u32(sK);
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          const uint32_t at = x / 4 * C::ATOM + x % 4 * 32;
+          umma_f16_ss(tmem + t * kKvTileTokens, smem_desc_k_sw128(q + at),
+                      smem_desc_k_sw128(k + at), idesc_s, x != 0);
+        }
+        umma_commit(&s_full[t]);
+      };
+      auto sums = [&](int t, int j) {  // O_t += P_t V
+        const uint32_t v = smem_u32(sV + (j & 1) * C::TILE);
+#pragma unroll
+        for (int x = 0; x < kKvTileTokens / 16; ++x)
+          umma_f16_ts(tmem + C::O_COL + t * 128, tmem + t * kKvTileTokens + x * 8,
+                      smem_desc_mn_sw128(v + x * 2048, C::ATOM), idesc_o, (j | x) != 0);
+        umma_commit(&pv_done[t]);
+      };
+      bool ok = wait(&k_full, 0);
+      if (ok) {
+        for (int t = 0; t < row_tiles; ++t) scores(t);
+        umma_commit(&k_empty);
+      }
+      for (int j = 0; j < tiles && ok; ++j) {
+        ok = wait(&v_full[j & 1], j >> 1);
+        const bool more = j + 1 < tiles;
+        for (int t = 0; t < row_tiles && ok; ++t) {
+          ok = wait(&p_full[t], j);
+          if (!ok) break;
+          sums(t, j);
+          if (t == row_tiles - 1) umma_commit(&v_empty[j & 1]);
+          if (!more) continue;
+          if (t == 0) ok = wait(&k_full, j + 1);
+          // P_t lies where S_t goes
+          if (ok) ok = wait(&pv_done[t], j);
+          if (!ok) break;
+          scores(t);
+          if (t == row_tiles - 1) umma_commit(&k_empty);
+        }
+      }
+      umma_commit(&drain);
+      int zero = 0;
+      if (!mbar_wait_bounded(&drain, 0, &zero, timeout_ns)) record_timeout(kSiteKvTiles);
+    }
+    __syncwarp();
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------ codes to FP16
+    const int w = warp - 12;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, int n) {
+      if (mbar_wait_polled_warp(bar, n & 1, abort_flag, timeout_ns)) return true;
+      if (lane == 0) {
+        record_timeout(kSiteKvTiles);
+        *abort_flag = 1;
+      }
+      return false;
+    };
+    // this warp's two strips (32 tokens) of K or V
+    auto convert = [&](const uint8_t *raw, uint8_t *tile, bool is_v, int tok0, uint32_t gone) {
+      constexpr int LANES = D / 32;      // lanes of a row, 32 elements (16 bytes of codes) each
+      constexpr int ROWS = 32 / LANES;   // rows of a round
+      const int part = lane % LANES;
+#pragma unroll
+      for (int x = 0; x < 32 / ROWS; ++x) {
+        const int row = w * 32 + x * ROWS + lane / LANES;  // in the tile
+        const int in = row % kStripTokens;
+        const uint8_t *strip = raw + row / kStripTokens * strip_bytes(D);
+        const uint4 codes = *reinterpret_cast<const uint4 *>(strip + (is_v ? strip_v(D) : 0) +
+                                                             in * (D / 2) + part * 16);
+        uint32_t sc = *reinterpret_cast<const uint16_t *>(
+            strip + (is_v ? strip_vs(D) : strip_ks(D)) + in * (D / 16) + part * 2);
+        // V of tokens that are not there has to be finite: rows weigh it with 0
+        if (is_v && (tok0 + row >= req.kv || (gone >> (row / kStripTokens) & 1u))) sc = 0;
+        const uint32_t sh = cvt_f16_e4m3x2(sc);
+        const __half2 s = *reinterpret_cast<const __half2 *>(&sh);
+        const __half2 s0 = __low2half2(s), s1 = __high2half2(s);
+        uint32_t h[4][4];
+        cvt_f16_e2m1x8(codes.x, h[0]);
+        cvt_f16_e2m1x8(codes.y, h[1]);
+        cvt_f16_e2m1x8(codes.z, h[2]);
+        cvt_f16_e2m1x8(codes.w, h[3]);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+#pragma unroll
+          for (int z = 0; z < 4; ++z) h[y][z] = scaled(h[y][z], y < 2 ? s0 : s1);
+        }
+        // 16-byte units 4 (part % 2) + y of the row's 128 bytes in atom part / 2,
+        // swizzled; the second atom's lanes go in another order, which keeps
+        // the eight lanes of a store phase on eight different units
+        uint8_t *to = tile + part / 2 * C::ATOM + row * 128;
+        const int turn = part / 2 * 2;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int unit = part % 2 * 4 + (y ^ turn);
+          const uint4 v = turn ? make_uint4(h[y ^ 2][0], h[y ^ 2][1], h[y ^ 2][2], h[y ^ 2][3])
+                               : make_uint4(h[y][0], h[y][1], h[y][2], h[y][3]);
+          *reinterpret_cast<uint4 *>(to + ((unit ^ (row & 7)) << 4)) = v;
+        }
+      }
+    };
+    for (int j = 0; j < tiles && ok; ++j) {
+      const int slot = j & 1;
+      const uint8_t *raw = sRaw + slot * C::RAW_PAD;
+      const int tok0 = j * kKvTileTokens;
+      ok = wait(&raw_full[slot], j >> 1);
+      if (!ok) break;
+      const uint32_t gone = missing[j % kKvMasks];
+      ok = wait(&k_empty, j + 1);  // the products with the K before are done
+      if (!ok) break;
+      convert(raw, sK, false, tok0, gone);
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_full);
+      ok = wait(&v_empty[slot], (j >> 1) + 1);
+      if (!ok) break;
+      convert(raw, sV + slot * C::TILE, true, tok0, gone);
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&v_full[slot]);
+        mbar_arrive(&raw_empty[slot]);
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax
+    const int tile = (warp - 4) / 4, quarter = warp & 3;
+    const int r = tile * 128 + quarter * 32 + lane;  // this thread's row of the block
+    const bool live = r < rows;
+    const int i = live ? (row0 + r) / a.group : 0;
+    const int64_t at = (static_cast<int64_t>(req.q0 + i) * a.cache.heads + head) * a.group +
+                       (row0 + r) % a.group;
+    const int lim = live ? kv_limit(req, i, a.causal) : most;
+    const float factor = a.scale * 1.4426950408889634f * __ldg(a.s_k);
+    float c = 0.0f;  // scores to log2 units, never negative
+    {
+      uint4 q[D / 8];
+      uint32_t top = 0;
+#pragma unroll
+      for (int x = 0; x < D / 8; ++x) {
+        q[x] = live ? __ldg(reinterpret_cast<const uint4 *>(a.q + at * D) + x)
+                    : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {q[x].x, q[x].y, q[x].z, q[x].w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) top = max(top, max(w[y] & 0x7FFFu, (w[y] >> 16) & 0x7FFFu));
+      }
+      const int e = top == 0 ? 0 : min(max(static_cast<int>(top >> 7) - 127, -126), 126);
+      c = fabsf(factor) * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      const float down =
+          copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), factor);
+      uint8_t *to = sQ + tile * C::TILE + (quarter * 32 + lane) * 128;
+#pragma unroll
+      for (int x = 0; x < D / 8; ++x) {
+        const uint4 h = make_uint4(pack_f16(bf16_lo(q[x].x) * down, bf16_hi(q[x].x) * down),
+                                   pack_f16(bf16_lo(q[x].y) * down, bf16_hi(q[x].y) * down),
+                                   pack_f16(bf16_lo(q[x].z) * down, bf16_hi(q[x].z) * down),
+                                   pack_f16(bf16_lo(q[x].w) * down, bf16_hi(q[x].w) * down));
+        *reinterpret_cast<uint4 *>(to + x / 8 * C::ATOM + (((x % 8) ^ (lane & 7)) << 4)) = h;
+      }
+      fence_async_shared();
+    }
+    asm volatile("bar.sync 1, 288;" ::: "memory");  // with the MMA warp
+    const bool used = tile < row_tiles;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t t_s = tmem + lanes + tile * kKvTileTokens;
+    const uint32_t t_o = tmem + lanes + C::O_COL + tile * 128;
+    float neg_m = INFINITY, l = 0.0f;  // minus the maximum in log2 units, the sum
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, int n) {
+      if (mbar_wait_polled_warp(bar, n & 1, abort_flag, timeout_ns)) return true;
+      if (lane == 0) {
+        record_timeout(kSiteKvTiles);
+        *abort_flag = 1;
+      }
+      return false;
+    };
+    for (int j = 0; used && j < tiles; ++j) {
+      ok = wait(&s_full[tile], j);
+      if (!ok) break;
+      tc_fence_after();
+      const int tok0 = j * kKvTileTokens;
+      const uint32_t gone = missing[j % kKvMasks];
+      const bool edge =
+          __any_sync(0xFFFFFFFFu, tok0 + kKvTileTokens > lim) || gone != 0;
+      // a score that the row does not see is -inf
+      auto masked = [&](uint32_t (&s)[32], int col) {
+#pragma unroll
+        for (int x = 0; x < 32; ++x)
+          if (tok0 + col + x >= lim || (gone >> ((col + x) / kStripTokens) & 1u))
+            s[x] = 0xFF800000u;
+      };
+      float top = -INFINITY;
+#pragma unroll
+      for (int col = 0; col < kKvTileTokens; col += 32) {
+        uint32_t s[32];
+        tmem_ld_32x32b_x32(t_s + col, s);
+        tmem_ld_wait();
+        if (edge) masked(s, col);
+#pragma unroll
+        for (int x = 0; x < 32; ++x) top = fmaxf(top, __uint_as_float(s[x]));
+      }
+      const float now = top == -INFINITY ? -INFINITY : top * c;
+      if (__any_sync(0xFFFFFFFFu, now + neg_m > kKvSlack)) {
+        // move the maxima (at first from -inf); O must not be in use
+        const float next = fmaxf(-neg_m, now);
+        const float by = next == -INFINITY ? 1.0f : ex2_approx(-neg_m - next);
+        neg_m = next == -INFINITY ? INFINITY : -next;
+        l *= by;
+        if (j > 0) {
+          ok = wait(&pv_done[tile], j - 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int col = 0; col < D; col += 32) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(t_o + col, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * by);
+            tmem_st_32x32b_x32(t_o + col, o);
+          }
+        }
+      }
+      // weights; chunk by chunk P takes the columns of scores already read
+#pragma unroll
+      for (int col = 0; col < kKvTileTokens; col += 32) {
+        uint32_t s[32], p[16];
+        tmem_ld_32x32b_x32(t_s + col, s);
+        tmem_ld_wait();
+        float part[2] = {0.0f, 0.0f};
+        if (edge) {
+          masked(s, col);
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            const bool unseen = s[x] == 0xFF800000u;
+            s[x] = unseen ? 0u
+                          : __float_as_uint(ex2_approx(fmaf(__uint_as_float(s[x]), c, neg_m)));
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            s[x] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(s[x]), c, neg_m)));
+        }
+#pragma unroll
+        for (int x = 0; x < 32; ++x) part[x & 1] += __uint_as_float(s[x]);
+        l += part[0] + part[1];
+        // P is rounded to FP16 (2^-11 of each weight) for the second product
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          p[x] = pack_f16(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
+        tmem_st_32x32b_x16(t_s + col / 2, p);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[tile]);
+    }
+    if (used && ok && tiles > 0) {
+      ok = wait(&pv_done[tile], tiles - 1);
+      tc_fence_after();
+    }
+    if (used && ok) {
+      const float s_v = a.s_out ? __ldg(a.s_v) / __ldg(a.s_out) : __ldg(a.s_v);
+      const float by = l != 0.0f ? s_v / l : 0.0f;
+#pragma unroll 1
+      for (int col = 0; col < D; col += 32) {
+        uint32_t o[32];
+        if (tiles > 0) {
+          tmem_ld_32x32b_x32(t_o + col, o);
+          tmem_ld_wait();
+        }
+#pragma unroll
+        for (int x = 0; x < 32; x += 8) {
+          float v[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            v[y] = tiles > 0 && l != 0.0f ? __uint_as_float(o[x + y]) * by : 0.0f;
+          if (!live) continue;
+          if (a.s_out) {
+            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + at * D + col + x) =
+                make_uint2(pack4(cvt_e4m3x2(v[0], v[1]), cvt_e4m3x2(v[2], v[3])),
+                           pack4(cvt_e4m3x2(v[4], v[5]), cvt_e4m3x2(v[6], v[7])));
+          } else {
+            uint32_t h[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const __nv_bfloat162 z = __floats2bfloat162_rn(v[2 * y], v[2 * y + 1]);
+              h[y] = *reinterpret_cast<const uint32_t *>(&z);
+            }
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at * D + col + x) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        }
+      }
+      if (a.lse && live) a.lse[at] = (log2f(l) - neg_m) * 0.6931471805599453f;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace fp8ws

@@ -9,6 +9,7 @@
 // in a small ring for tests and benchmarks.
 #include "../../include/fp8ws.h"
 
+#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 #include <stdlib.h>
@@ -20,6 +21,7 @@
 #include "common.cuh"
 #include "elementwise.cuh"
 #include "fp4_attention.cuh"
+#include "fp4_attention_tiles.cuh"
 #include "fp4_kv.cuh"
 #include "gemm_dual_sm100.cuh"
 #include "gemm_epilogue_sm100.cuh"
@@ -73,7 +75,8 @@ struct DeviceInfo {
   // 3/5/6/7 pair GEMM scale modes (+16 direct-store), 9 five-stage pair GEMM,
   // 4 dual (+8 variant, +16 direct variant, +24 direct plain), 8 per-token SwiGLU,
   // 10 staged quantizer, 32-35 attention over the 4-bit cache (few rows),
-  // 36-39 Linear with a fused epilogue
+  // 36-39 Linear with a fused epilogue, 40-41 attention over
+  // the 4-bit cache (many rows)
   std::atomic<uint64_t> gemm_attr_set{0};
   std::atomic<int> pair_clusters{0};  // CTA pairs of the pair GEMM resident at once
   std::atomic<int> dual_clusters{0};  // CTA pairs of the gate/up dual GEMM resident at once
@@ -1003,6 +1006,34 @@ int launch_kv_rows(DeviceInfo *d, KvAttnArgs a, cudaStream_t st) {
   return launch_status();
 }
 
+// Requests of up to this many rows (tokens x query heads of a K/V head) go to
+// fp4_kv_rows_kernel, of more to fp4_kv_tiles_kernel.
+constexpr int kKvFewRows = 32;
+
+template <int D, int BIT>
+int launch_kv_tiles(DeviceInfo *d, const KvAttnArgs &a, cudaStream_t st) {
+  using C = KvTilesCfg<D>;
+  auto kern = fp4_kv_tiles_kernel<D>;
+  int rc = once_per_device(d, BIT, [&] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) ==
+                   cudaSuccess
+               ? FP8WS_OK
+               : FP8WS_ERR_CUDA;
+  });
+  if (rc) return rc;
+  // 256-row blocks there can be: one begun by each request of more than
+  // few_rows rows beside the full ones
+  const int64_t rows = static_cast<int64_t>(a.total_q) * a.group;
+  const int64_t begun = rows / (a.few_rows + 1);
+  const int64_t blocks = a.cache.heads * (rows / kKvTileRows + (begun < a.batch ? begun : a.batch));
+  if (blocks == 0) return FP8WS_OK;
+  if (launch_ex(kern, dim3(static_cast<unsigned>(blocks)), dim3(kKvTileThreads), C::SMEM, st, 1, a,
+                kWaitLimitNs) != cudaSuccess)
+    return FP8WS_ERR_CUDA;
+  log_launch(kKindKvAttention, a.q, a.cache.data, a.out);
+  return launch_status();
+}
+
 }  // namespace
 }  // namespace fp8ws
 
@@ -1786,18 +1817,24 @@ int fp4_kv_attention(const uint16_t *q, int64_t total_q, int64_t q_heads, int64_
   if (total_q == 0 || batch == 0 || max_q == 0) return FP8WS_OK;
   const size_t part_bytes =
       round256(static_cast<size_t>(2 * kKvMaxBlocks) * 16 * (128 + 2) * sizeof(float));
-  const KvAttnArgs a{q, static_cast<int>(total_q), static_cast<int>(batch),
+  KvAttnArgs a{q, static_cast<int>(total_q), static_cast<int>(batch),
                      static_cast<int>(q_heads / kv_heads), cu_q, kv_lens, block_table, table_width,
                      KvCache{const_cast<uint8_t *>(cache), num_pages, static_cast<int>(kv_heads),
                              page_shift(page_size)},
-                     s_k, s_v, scale, causal ? 1 : 0, s_out, out, lse,
+                     s_k, s_v, scale, causal ? 1 : 0, kKvFewRows, s_out, out, lse,
                      static_cast<float *>(workspace),
                      reinterpret_cast<int4 *>(static_cast<uint8_t *>(workspace) + part_bytes)};
-  const bool few = max_q * (q_heads / kv_heads) <= 8;
+  const int64_t most = max_q * (q_heads / kv_heads);  // rows of a request
   cudaStream_t st = as_stream(stream);
+  if (most > kKvFewRows) {
+    rc = head_dim == 128 ? launch_kv_tiles<128, 40>(d, a, st) : launch_kv_tiles<64, 41>(d, a, st);
+    if (rc) return rc;
+  } else {
+    a.few_rows = INT_MAX;  // should a request have more than max_q rows after all
+  }
   if (head_dim == 128)
-    return few ? launch_kv_rows<128, 1, 32>(d, a, st) : launch_kv_rows<128, 2, 33>(d, a, st);
-  return few ? launch_kv_rows<64, 1, 34>(d, a, st) : launch_kv_rows<64, 2, 35>(d, a, st);
+    return most <= 8 ? launch_kv_rows<128, 1, 32>(d, a, st) : launch_kv_rows<128, 2, 33>(d, a, st);
+  return most <= 8 ? launch_kv_rows<64, 1, 34>(d, a, st) : launch_kv_rows<64, 2, 35>(d, a, st);
 }
 
 int fp8_check_shared_input_scale(const float *const *d_scales, int n, void *stream) {

@@ -753,7 +753,8 @@ FP8WS_API int fp8ws_device_check(void);
  * accumulator), 4 (epilogue, finished accumulator), 5 (teardown, last MMAs);
  * 6 the self-test below; in the staged quantizer 7 (consumers, loaded chunk),
  * 8 (producer, free slot); 9 attention over the 4-bit cache (strips of the
- * cache), 10 the Linear with a fused epilogue (a residual box). */
+ * cache), few rows, 10 the Linear with a fused epilogue (a residual box), 11
+ * attention over the 4-bit cache, many rows. */
 FP8WS_API int fp8ws_device_status(int *status, int *where);
 
 /* Self-test of the bounded waits every GEMM kernel uses (failure detection
