@@ -94,67 +94,128 @@ __device__ __forceinline__ int64_t strip_offset(const KvCache &c, int64_t slot, 
 }
 
 // ------------------------------------------------------------------ append
-// One token's head takes D/4 lanes: D/8 for K, D/8 for V, 8 values each, so
-// that K's and V's loads of a warp are whole 128-byte lines.  A pair of lanes
-// owns the 16 values of a scale.
+// A lane owns the 16 values of a scale, so nothing is exchanged but the NaN
+// ballot: D/16 lanes for a token's K of one head, D/16 for its V.  Bound by the
+// values' bytes (2 read, 0.56 written).  An IEEE division per value would cost
+// more than the stream (26 us for 8191 x 8 x 128 with it), so a code is first
+// bracketed: with r = fl32(1 / by), x fl32(r (1 - 2^-20)) and x fl32(r (1 +
+// 2^-20)) lie on either side of fl32(x / by) (each of their two roundings, and
+// the quotient's, is 2^-24); where both have one code it is the quotient's, and
+// only lanes with a code that differs divide.
+constexpr int kKvUnroll = 2;  // units in flight per lane
+
+// Codes of x[8] / by, the IEEE quotient's.  r is 1 / by, 0 to divide at once.
+__device__ __forceinline__ uint32_t quotient_codes(const float (&x)[8], float by, float r) {
+  const float lo = __fmul_rn(r, 1.0f - 0x1p-20f), hi = __fmul_rn(r, 1.0f + 0x1p-20f);
+  float p[8], q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    p[i] = __fmul_rn(x[i], lo);
+    q[i] = __fmul_rn(x[i], hi);
+  }
+  const uint32_t a = cvt_e2m1x8(p), b = cvt_e2m1x8(q);
+  if (a == b && r != 0.0f) return a;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) p[i] = __fdiv_rn(x[i], by);
+  return cvt_e2m1x8(p);
+}
+
+// One token's K or V of 16 values (two 16-byte vectors) -> 8 bytes of codes and
+// the scale's code.  NaN values count as 0 (`nan` tells).
+__device__ __forceinline__ uint2 quantize16(const uint4 (&w)[2], float s, float s6,
+                                            uint32_t &scale, bool &nan) {
+  uint32_t raw[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+  auto largest = [&] {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = __vmaxu2(top, raw[i] & 0x7FFF7FFFu);
+    return max(top & 0xFFFFu, top >> 16);
+  };
+  uint32_t top = largest();
+  nan = top > 0x7F80u;
+  if (nan) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((raw[i] & 0x7FFFu) > 0x7F80u) raw[i] &= 0xFFFF0000u;
+      if ((raw[i] >> 16 & 0x7FFFu) > 0x7F80u) raw[i] &= 0x0000FFFFu;
+    }
+    top = largest();
+  }
+  scale = cvt_e4m3x2(__fdiv_rn(__uint_as_float(top << 16), s6), 0.0f) & 0xFFu;
+  const float by = __fmul_rn(e4m3_to_float(scale), s);
+  if (!(by > 0.0f)) return make_uint2(0, 0);
+  const float r = by > 0x1p-120f && by < 0x1p120f ? __frcp_rn(by) : 0.0f;
+  uint2 codes;
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf16_lo(raw[i]);
+    x[2 * i + 1] = bf16_hi(raw[i]);
+  }
+  codes.x = quotient_codes(x, by, r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf16_lo(raw[4 + i]);
+    x[2 * i + 1] = bf16_hi(raw[4 + i]);
+  }
+  codes.y = quotient_codes(x, by, r);
+  return codes;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kKvThreads)
     fp4_kv_append_kernel(const uint16_t *__restrict__ k, const uint16_t *__restrict__ v,
                          const int64_t *__restrict__ slots, int64_t units, const float *s_k,
                          const float *s_v, const KvCache c) {
-  constexpr int LANES = D / 4;
+  constexpr int LANES = D / 8;             // lanes of a unit: one token of one head
+  constexpr int UNITS = kKvThreads / LANES;  // units of a block's round
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x % LANES;
   const bool is_v = lane >= LANES / 2;
-  const int part = lane % (LANES / 2);  // which 8 values
+  const int part = lane % (LANES / 2);  // which 16 values
   const float s = __ldg(is_v ? s_v : s_k);
   const float s6 = __fmul_rn(6.0f, s);
   const int64_t n_slots = c.pages << c.page_shift;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * (kKvThreads / LANES);
-  const int64_t warp_units = 32 / LANES;
-  // every lane of a warp runs the same number of rounds (the shuffles below)
-  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * (kKvThreads / LANES) +
-                    (threadIdx.x / 32) * warp_units;
-       u0 < units; u0 += stride) {
-    const int64_t u = u0 + (threadIdx.x % 32) / LANES;
-    const bool live = u < units;
-    const int64_t token = live ? u / c.heads : 0;
-    const int head = live ? static_cast<int>(u - token * c.heads) : 0;
-    const int64_t slot = live ? __ldg(slots + token) : -1;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (live) w = ld_stream(reinterpret_cast<const uint4 *>((is_v ? v : k) + u * D) + part);
-    float x[8] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y),
-                  bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w)};
-    float amax = 0.0f;
-    bool nan = false;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * UNITS;
+  const uint32_t mine = ((1u << LANES) - 1u) << (threadIdx.x % 32 / LANES * LANES);
+  const uint16_t *from = is_v ? v : k;
+  // every lane of a warp runs the same number of rounds (the ballots below)
+  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * UNITS; u0 < units;
+       u0 += kKvUnroll * stride) {
+    uint4 w[kKvUnroll][2];
+    int64_t slot[kKvUnroll];
+    int head[kKvUnroll];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (x[i] != x[i]) {
-        nan = true;
-        x[i] = 0.0f;
+    for (int x = 0; x < kKvUnroll; ++x) {
+      const int64_t u = u0 + x * stride + threadIdx.x / LANES;
+      w[x][0] = w[x][1] = make_uint4(0, 0, 0, 0);
+      slot[x] = -1;
+      head[x] = 0;
+      if (u < units) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(from + u * D) + 2 * part;
+        w[x][0] = ld_stream(src);
+        w[x][1] = ld_stream(src + 1);
+        const int64_t token = units <= INT32_MAX ? static_cast<uint32_t>(u) / c.heads : u / c.heads;
+        head[x] = static_cast<int>(u - token * c.heads);
+        slot[x] = __ldg(slots + token);
       }
-      amax = fmaxf(amax, fabsf(x[i]));
     }
-    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-    const uint32_t nans = __ballot_sync(0xFFFFFFFFu, nan);
-    const uint32_t mine = (LANES == 32 ? 0xFFFFFFFFu : ((1u << LANES) - 1u))
-                          << ((threadIdx.x % 32) / LANES * LANES);
-    uint32_t scale = cvt_e4m3x2(__fdiv_rn(amax, s6), 0.0f) & 0xFFu;
-    const float by = __fmul_rn(e4m3_to_float(scale), s);
-    float t[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = by > 0.0f ? __fdiv_rn(x[i], by) : 0.0f;
-    const uint32_t codes = cvt_e2m1x8(t);
-    if (!is_v && (nans & mine)) scale = 0x7Fu;
-    if (slot < 0 || slot >= n_slots) continue;
-    uint8_t *strip = c.data + strip_offset<D>(c, slot, head);
-    const int row = static_cast<int>(slot & (kStripTokens - 1));
-    *reinterpret_cast<uint32_t *>(strip + (is_v ? strip_v(D) : 0) + row * (D / 2) + part * 4) =
-        codes;
-    if (!(part & 1))
-      strip[(is_v ? strip_vs(D) : strip_ks(D)) + row * (D / 16) + part / 2] =
+    for (int x = 0; x < kKvUnroll; ++x) {
+      uint32_t scale;
+      bool nan;
+      const uint2 codes = quantize16(w[x], s, s6, scale, nan);
+      const uint32_t nans = __ballot_sync(0xFFFFFFFFu, nan);
+      if (!is_v && (nans & mine)) scale = 0x7Fu;
+      if (slot[x] < 0 || slot[x] >= n_slots) continue;
+      uint8_t *strip = c.data + strip_offset<D>(c, slot[x], head[x]);
+      const int row = static_cast<int>(slot[x] & (kStripTokens - 1));
+      *reinterpret_cast<uint2 *>(strip + (is_v ? strip_v(D) : 0) + row * (D / 2) + part * 8) =
+          codes;
+      strip[(is_v ? strip_vs(D) : strip_ks(D)) + row * (D / 16) + part] =
           static_cast<uint8_t>(scale);
+    }
   }
 }
 
@@ -164,7 +225,8 @@ __global__ void __launch_bounds__(kKvThreads)
     fp4_kv_gather_kernel(const int64_t *__restrict__ slots, int64_t units, const float *s_k,
                          const float *s_v, const KvCache c, uint16_t *__restrict__ k,
                          uint16_t *__restrict__ v) {
-  constexpr int LANES = D / 4;
+  constexpr int LANES = D / 8;
+  constexpr int UNITS = kKvThreads / LANES;
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x % LANES;
@@ -172,45 +234,67 @@ __global__ void __launch_bounds__(kKvThreads)
   const int part = lane % (LANES / 2);
   const float s = __ldg(is_v ? s_v : s_k);
   const int64_t n_slots = c.pages << c.page_shift;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * (kKvThreads / LANES);
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kKvThreads / LANES) + threadIdx.x / LANES;
-       u < units; u += stride) {
-    const int64_t token = u / c.heads;
-    const int head = static_cast<int>(u - token * c.heads);
-    const int64_t slot = __ldg(slots + token);
-    uint4 out = make_uint4(0, 0, 0, 0);
-    if (slot >= 0 && slot < n_slots) {
-      const uint8_t *strip = c.data + strip_offset<D>(c, slot, head);
-      const int row = static_cast<int>(slot & (kStripTokens - 1));
-      const uint32_t codes = *reinterpret_cast<const uint32_t *>(
-          strip + (is_v ? strip_v(D) : 0) + row * (D / 2) + part * 4);
-      const float scale =
-          e4m3_to_float(strip[(is_v ? strip_vs(D) : strip_ks(D)) + row * (D / 16) + part / 2]);
-      uint32_t h[4], r[4];
-      cvt_f16_e2m1x8(codes, h);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * UNITS;
+  uint16_t *to = is_v ? v : k;
+  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * UNITS + threadIdx.x / LANES; u0 < units;
+       u0 += kKvUnroll * stride) {
+    uint2 codes[kKvUnroll];
+    uint32_t scale[kKvUnroll];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<__half2 *>(&h[i]));
-        // code x scale is exact; two roundings, to fp32 and to BF16
-        const __nv_bfloat162 b =
-            __floats2bfloat162_rn((f.x * scale) * s, (f.y * scale) * s);
-        r[i] = *reinterpret_cast<const uint32_t *>(&b);
+    for (int x = 0; x < kKvUnroll; ++x) {
+      const int64_t u = u0 + x * stride;
+      codes[x] = make_uint2(0, 0);
+      scale[x] = 0;  // zeros for a slot outside the cache
+      if (u < units) {
+        const int64_t token = units <= INT32_MAX ? static_cast<uint32_t>(u) / c.heads : u / c.heads;
+        const int head = static_cast<int>(u - token * c.heads);
+        const int64_t slot = __ldg(slots + token);
+        if (slot >= 0 && slot < n_slots) {
+          const uint8_t *strip = c.data + strip_offset<D>(c, slot, head);
+          const int row = static_cast<int>(slot & (kStripTokens - 1));
+          codes[x] = *reinterpret_cast<const uint2 *>(strip + (is_v ? strip_v(D) : 0) +
+                                                      row * (D / 2) + part * 8);
+          scale[x] = strip[(is_v ? strip_vs(D) : strip_ks(D)) + row * (D / 16) + part];
+        }
       }
-      out = make_uint4(r[0], r[1], r[2], r[3]);
     }
-    st_stream(reinterpret_cast<uint4 *>((is_v ? v : k) + u * D) + part, out);
+#pragma unroll
+    for (int x = 0; x < kKvUnroll; ++x) {
+      const int64_t u = u0 + x * stride;
+      if (u >= units) break;
+      const float f = e4m3_to_float(scale[x]);
+      uint32_t h[2][4], r[2][4];
+      cvt_f16_e2m1x8(codes[x].x, h[0]);
+      cvt_f16_e2m1x8(codes[x].y, h[1]);
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 e = __half22float2(*reinterpret_cast<__half2 *>(&h[y][i]));
+          // code x scale is exact; two roundings, to fp32 and to BF16
+          const __nv_bfloat162 b = __floats2bfloat162_rn((e.x * f) * s, (e.y * f) * s);
+          r[y][i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+      uint4 *dst = reinterpret_cast<uint4 *>(to + u * D) + 2 * part;
+      st_stream(dst, make_uint4(r[0][0], r[0][1], r[0][2], r[0][3]));
+      st_stream(dst + 1, make_uint4(r[1][0], r[1][1], r[1][2], r[1][3]));
+    }
   }
 }
 
 // ------------------------------------------------------------------ tables
-// Block tables, row offsets and slots of one step, in one cluster: its first
-// block scans the requests' lengths (each thread one request, a running sum
-// from one 512-request round to the next), writes the row offsets, the new
-// lengths and the table entries of the new pages; after a cluster barrier
-// every thread of the cluster finds the slots of its tokens by a search in the
-// row offsets.  All of it is latency: a few dependent reads of a few KB.
-constexpr int kTableThreads = 512;
+// Block tables, row offsets and slots of one step, in one cluster.  Every
+// block scans the requests' lengths, a thread a request and THREADS at a time
+// (the same few KB, so no block waits for another's sums), and fills the new
+// pages of its share of the requests, a warp a request.  After a cluster
+// barrier the warps take 256 slots at a time: the requests of the first and the
+// last of them bound the search of the others (one request, or two or three,
+// for prompts).  The row offsets are searched in shared memory where one round
+// covers the batch.  All of it is latency, not bytes: dependent reads and the
+// instructions of a few SMs are what it counts (300 prompts, 80 thousand
+// tokens: 36 us with a full search per slot and one block filling the pages).
 constexpr int kTableMaxBlocks = 8;  // the portable cluster size
+constexpr int kTableUnroll = 8;     // slots of a thread in flight
 
 struct TableArgs {
   const int32_t *lens;
@@ -234,102 +318,146 @@ __device__ __forceinline__ int64_t pages_of(int64_t tokens, int shift, int64_t w
   return p < width ? p : width;
 }
 
-__global__ void __launch_bounds__(kTableThreads) fp4_kv_tables_kernel(const TableArgs a) {
-  __shared__ int64_t warp_rows[kTableThreads / 32], warp_pages[kTableThreads / 32];
+__device__ __forceinline__ int32_t saturate_i32(int64_t v) {
+  return static_cast<int32_t>(v < INT32_MAX ? v : INT32_MAX);
+}
+
+// The first of requests [lo, hi) whose rows end after t (hi: none).
+__device__ __forceinline__ int request_of(const int32_t *cu, int t, int lo, int hi) {
+  while (lo < hi) {
+    const int mid = lo + (hi - lo) / 2;
+    if (cu[mid + 1] > t)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) fp4_kv_tables_kernel(const TableArgs a) {
+  constexpr int WARPS = THREADS / 32;
+  __shared__ int64_t warp_rows[WARPS], warp_pages[WARPS];
+  __shared__ int64_t s_from[THREADS];  // a request's first new page in free_pages
+  __shared__ int32_t s_held[THREADS], s_need[THREADS];
+  __shared__ int32_t s_cu[THREADS + 1], s_old[THREADS];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  if (cluster_ctarank() == 0) {
-    const int64_t used = max(0, *a.used);
-    int64_t rows = 0, pages = 0;  // of the requests before this round
-    if (threadIdx.x == 0) a.cu_q[0] = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += kTableThreads) {
-      const int b = b0 + static_cast<int>(threadIdx.x);
-      int64_t old = 0, add = 0;
-      if (b < a.batch) {
-        old = max(0, a.lens[b]);
-        add = max(0, a.added[b]);
-      }
-      const int64_t held = pages_of(old, a.page_shift, a.width);
-      const int64_t need = pages_of(old + add, a.page_shift, a.width) - held;
-      int64_t r = add, p = need;  // inclusive sums over the warp, then the block
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int64_t r2 = __shfl_up_sync(0xFFFFFFFFu, r, d);
-        const int64_t p2 = __shfl_up_sync(0xFFFFFFFFu, p, d);
-        if (lane >= d) {
-          r += r2;
-          p += p2;
-        }
-      }
-      if (lane == 31) {
-        warp_rows[warp] = r;
-        warp_pages[warp] = p;
-      }
-      __syncthreads();
-      int64_t all_rows = 0, all_pages = 0;
-#pragma unroll
-      for (int w = 0; w < kTableThreads / 32; ++w) {
-        if (w < warp) {
-          r += warp_rows[w];
-          p += warp_pages[w];
-        }
-        all_rows += warp_rows[w];
-        all_pages += warp_pages[w];
-      }
-      __syncthreads();
-      if (b < a.batch) {
-        a.cu_q[b + 1] = static_cast<int32_t>(min(rows + r, static_cast<int64_t>(INT32_MAX)));
-        a.kv_lens[b] = static_cast<int32_t>(min(old + add, static_cast<int64_t>(INT32_MAX)));
-      }
-      // the new pages of the warp's requests, one request after the other
-      const int64_t first = used + pages + p - need;
-      uint32_t todo = __ballot_sync(0xFFFFFFFFu, need > 0);
-      while (todo) {
-        const int src = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const int64_t n = __shfl_sync(0xFFFFFFFFu, need, src);
-        const int64_t from = __shfl_sync(0xFFFFFFFFu, first, src);
-        const int64_t to = __shfl_sync(0xFFFFFFFFu, held, src);
-        int32_t *row = a.table + static_cast<int64_t>(b0 + warp * 32 + src) * a.width;
-        for (int64_t i = lane; i < n; i += 32)
-          row[to + i] = from + i < a.n_free ? a.free_pages[from + i] : -1;
-      }
-      rows += all_rows;
-      pages += all_pages;
+  const int rank = blockIdx.x, ranks = gridDim.x;
+  const int64_t used = max(0, *a.used);
+  int64_t rows = 0, pages = 0;  // of the requests before this round
+  for (int b0 = 0; b0 < a.batch; b0 += THREADS) {
+    const int b = b0 + static_cast<int>(threadIdx.x);
+    int64_t old = 0, add = 0;
+    if (b < a.batch) {
+      old = max(0, a.lens[b]);
+      add = max(0, a.added[b]);
     }
-    __syncthreads();  // pool may be the buffer that `used` was read from
-    if (threadIdx.x == 0) {
+    const int64_t held = pages_of(old, a.page_shift, a.width);
+    const int64_t need = pages_of(old + add, a.page_shift, a.width) - held;
+    int64_t r = add, p = need;  // inclusive sums over the warp, then the block
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t r2 = __shfl_up_sync(0xFFFFFFFFu, r, d);
+      const int64_t p2 = __shfl_up_sync(0xFFFFFFFFu, p, d);
+      if (lane >= d) {
+        r += r2;
+        p += p2;
+      }
+    }
+    if (lane == 31) {
+      warp_rows[warp] = r;
+      warp_pages[warp] = p;
+    }
+    // also: every block has read this round's lengths, which kv_lens may replace
+    cluster_sync();
+    int64_t all_rows = 0, all_pages = 0;
+#pragma unroll 8
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) {
+        r += warp_rows[w];
+        p += warp_pages[w];
+      }
+      all_rows += warp_rows[w];
+      all_pages += warp_pages[w];
+    }
+    s_from[threadIdx.x] = used + pages + p - need;
+    s_held[threadIdx.x] = static_cast<int32_t>(held);
+    s_need[threadIdx.x] = static_cast<int32_t>(need);
+    s_cu[threadIdx.x + 1] = saturate_i32(rows + r);
+    s_old[threadIdx.x] = static_cast<int32_t>(old);
+    if (rank == 0 && b < a.batch) {
+      a.cu_q[b + 1] = saturate_i32(rows + r);
+      a.kv_lens[b] = saturate_i32(old + add);
+    }
+    __syncthreads();
+    const int here = min(THREADS, a.batch - b0);
+    for (int x = rank * WARPS + warp; x < here; x += ranks * WARPS) {
+      const int n = s_need[x];
+      if (n == 0) continue;
+      const int64_t from = s_from[x];
+      int32_t *row = a.table + static_cast<int64_t>(b0 + x) * a.width + s_held[x];
+#pragma unroll 4
+      for (int i = lane; i < n; i += 32)
+        row[i] = from + i < a.n_free ? __ldg(a.free_pages + from + i) : -1;
+    }
+    rows += all_rows;
+    pages += all_pages;
+    __syncthreads();  // the shared arrays may be written again
+  }
+  if (threadIdx.x == 0) {
+    s_cu[0] = 0;
+    if (rank == 0) {
       const int64_t left = max(int64_t(0), a.n_free - used);
       const int64_t got = min(pages, left);
-      a.pool[0] = static_cast<int32_t>(min(used + got, static_cast<int64_t>(INT32_MAX)));
-      a.pool[1] = static_cast<int32_t>(min(pages - got, static_cast<int64_t>(INT32_MAX)));
+      a.cu_q[0] = 0;
+      a.pool[0] = saturate_i32(used + got);
+      a.pool[1] = saturate_i32(pages - got);
     }
   }
-  cluster_sync();  // the writes above are visible to the whole cluster
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kTableThreads + threadIdx.x; t < a.n_slots;
-       t += static_cast<int64_t>(gridDim.x) * kTableThreads) {
-    int lo = 0, hi = a.batch;  // the first request whose rows end after t
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (a.cu_q[mid + 1] > t)
-        hi = mid;
-      else
-        lo = mid + 1;
-    }
-    int64_t slot = -1;
-    if (lo < a.batch) {
-      const int64_t start = a.cu_q[lo];
-      // the request's new tokens are its last ones (lens may be kv_lens by now)
-      const int64_t at = a.kv_lens[lo] - static_cast<int64_t>(max(0, a.added[lo])) + t - start;
-      const int64_t j = at >> a.page_shift;
-      if (j < a.width) {
-        const int64_t page = a.table[static_cast<int64_t>(lo) * a.width + j];
-        if (page >= 0)
-          slot = (page << a.page_shift) + (at & ((int64_t(1) << a.page_shift) - 1));
+  cluster_sync();  // the entries and offsets above are visible to the whole cluster
+  const bool near = a.batch <= THREADS;  // the offsets are in shared memory
+  const int32_t *cu = near ? s_cu : a.cu_q;
+  const int last = min(a.n_slots, cu[a.batch]);  // slots behind have no token
+  constexpr int RUN = 32 * kTableUnroll;
+  for (int64_t base = static_cast<int64_t>(rank * WARPS + warp) * RUN; base < a.n_slots;
+       base += static_cast<int64_t>(ranks) * WARPS * RUN) {
+    const int t0 = static_cast<int>(base);
+    const int end = min(last - t0, RUN);  // slots of the run that have a token
+    // lane 0 the first slot's request, the others the last one's
+    int edge = 0;
+    if (end > 0) edge = request_of(cu, lane == 0 ? t0 : t0 + end - 1, 0, a.batch - 1);
+    const int b_first = __shfl_sync(0xFFFFFFFFu, edge, 0);
+    const int b_last = __shfl_sync(0xFFFFFFFFu, edge, 1);
+    int b[kTableUnroll];
+    int64_t at[kTableUnroll];
+    int32_t page[kTableUnroll];
+#pragma unroll
+    for (int x = 0; x < kTableUnroll; ++x) {
+      const int i = x * 32 + lane;
+      at[x] = -1;
+      b[x] = b_first;
+      if (i < end) {
+        b[x] = request_of(cu, t0 + i, b_first, b_last);
+        // the request's new tokens are its last ones (lens may be kv_lens by now)
+        const int64_t old = near ? s_old[b[x]]
+                                 : a.kv_lens[b[x]] - static_cast<int64_t>(max(0, a.added[b[x]]));
+        at[x] = old + (t0 + i - cu[b[x]]);
       }
     }
-    a.slots[t] = slot;
+#pragma unroll
+    for (int x = 0; x < kTableUnroll; ++x) {
+      const int64_t j = at[x] >> a.page_shift;
+      page[x] = at[x] >= 0 && j < a.width ? a.table[static_cast<int64_t>(b[x]) * a.width + j] : -1;
+    }
+#pragma unroll
+    for (int x = 0; x < kTableUnroll; ++x)
+      if (base + x * 32 + lane < a.n_slots)
+        a.slots[base + x * 32 + lane] =
+            page[x] < 0 ? -1
+                        : (static_cast<int64_t>(page[x]) << a.page_shift) +
+                              (at[x] & ((int64_t(1) << a.page_shift) - 1));
   }
 }
 

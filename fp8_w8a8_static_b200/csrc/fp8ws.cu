@@ -1698,7 +1698,7 @@ int fp4_kv_tables(const int32_t *lens, const int32_t *added, int64_t batch, int 
                   int64_t n_free, const int32_t *used, int32_t *pool, int32_t *cu_q,
                   int32_t *kv_lens, int64_t *slots, int64_t n_slots, void *stream) {
   const int shift = page_shift(page_size);
-  if (shift < 0 || batch < 0 || batch >= kLim31 - kTableThreads || table_width < 0 ||
+  if (shift < 0 || batch < 0 || batch >= kLim31 - 1024 || table_width < 0 ||
       table_width >= kLim31 || n_free < 0 || n_free >= kLim31 || n_slots < 0 || n_slots >= kLim31)
     return FP8WS_ERR_SHAPE;
   if (!used || !pool || !cu_q || (batch != 0 && (!lens || !added || !kv_lens)) ||
@@ -1711,11 +1711,19 @@ int fp4_kv_tables(const int32_t *lens, const int32_t *added, int64_t batch, int 
   const TableArgs a{lens,       added,  static_cast<int>(batch), shift, block_table,
                     table_width, free_pages, n_free, used, pool, cu_q, kv_lens, slots,
                     static_cast<int>(n_slots)};
-  // a second block pays once the slots take more than two rounds of the first
-  const int64_t want = (n_slots + 2 * kTableThreads - 1) / (2 * kTableThreads);
-  const int blocks = want < 1 ? 1 : (want < kTableMaxBlocks ? static_cast<int>(want) : kTableMaxBlocks);
-  if (launch_ex(fp4_kv_tables_kernel, dim3(blocks), dim3(kTableThreads), 0, as_stream(stream),
-                blocks, a) != cudaSuccess)
+  // A step's few requests: one block of 256 threads (3.4 against 5.7 us for 32
+  // requests with 1024).  Else blocks of 1024, one for each 2048 slots or 32
+  // requests, up to a cluster.
+  const bool few = batch <= 256 && n_slots <= 1024;
+  const int64_t by_slots = (n_slots + 2047) / 2048, by_requests = (batch + 31) / 32;
+  int64_t blocks = few ? 1 : (by_slots > by_requests ? by_slots : by_requests);
+  if (blocks < 1) blocks = 1;
+  if (blocks > kTableMaxBlocks) blocks = kTableMaxBlocks;
+  const int n = static_cast<int>(blocks);
+  cudaStream_t st = as_stream(stream);
+  if ((few ? launch_ex(fp4_kv_tables_kernel<256>, dim3(n), dim3(256), 0, st, n, a)
+           : launch_ex(fp4_kv_tables_kernel<1024>, dim3(n), dim3(1024), 0, st, n, a)) !=
+      cudaSuccess)
     return FP8WS_ERR_CUDA;
   log_launch(kKindKvCache, lens, added, slots);
   return launch_status();
@@ -1735,7 +1743,7 @@ int fp4_kv_append(const uint16_t *k, const uint16_t *v, int64_t tokens, int64_t 
   if (tokens == 0) return FP8WS_OK;
   const KvCache c{cache, num_pages, static_cast<int>(kv_heads), page_shift(page_size)};
   const int64_t units = tokens * kv_heads;
-  const int per_block = kKvThreads / (head_dim / 4);
+  const int per_block = kKvThreads / (head_dim / 8);
   cudaStream_t st = as_stream(stream);
   const cudaError_t e =
       head_dim == 128
@@ -1765,7 +1773,7 @@ int fp4_kv_gather(const uint8_t *cache, int64_t num_pages, int page_size, int64_
   const KvCache c{const_cast<uint8_t *>(cache), num_pages, static_cast<int>(kv_heads),
                   page_shift(page_size)};
   const int64_t units = tokens * kv_heads;
-  const int per_block = kKvThreads / (head_dim / 4);
+  const int per_block = kKvThreads / (head_dim / 8);
   cudaStream_t st = as_stream(stream);
   const cudaError_t e =
       head_dim == 128
