@@ -102,7 +102,7 @@ __device__ __forceinline__ int64_t strip_offset(const KvCache &c, int64_t slot, 
 // 2^-20)) lie on either side of fl32(x / by) (each of their two roundings, and
 // the quotient's, is 2^-24); where both have one code it is the quotient's, and
 // only lanes with a code that differs divide.
-constexpr int kKvUnroll = 2;  // units in flight per lane
+constexpr int kKvUnroll = 1;  // units in flight per lane
 
 // Codes of x[8] / by, the IEEE quotient's.  r is 1 / by, 0 to divide at once.
 __device__ __forceinline__ uint32_t quotient_codes(const float (&x)[8], float by, float r) {

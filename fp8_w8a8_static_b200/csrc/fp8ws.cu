@@ -26,6 +26,7 @@
 #include "gemm_dual_sm100.cuh"
 #include "gemm_epilogue_sm100.cuh"
 #include "gemm_pair_sm100.cuh"
+#include "gemm_rows_sm100.cuh"
 #include "gemm_sm100.cuh"
 
 namespace fp8ws {
@@ -76,11 +77,13 @@ struct DeviceInfo {
   // 4 dual (+8 variant, +16 direct variant, +24 direct plain), 8 per-token SwiGLU,
   // 10 staged quantizer, 32-35 attention over the 4-bit cache (few rows),
   // 36-39 Linear with a fused epilogue, 40-41 attention over
-  // the 4-bit cache (many rows)
+  // the 4-bit cache (many rows), 42-44 Linear with a fused epilogue (few rows)
   std::atomic<uint64_t> gemm_attr_set{0};
   std::atomic<int> pair_clusters{0};  // CTA pairs of the pair GEMM resident at once
   std::atomic<int> dual_clusters{0};  // CTA pairs of the gate/up dual GEMM resident at once
   // (the same for every epilogue variant: one CTA per SM either way)
+  // clusters of 2, 4, 8 blocks of each fp8_gemm_rows_kernel resident at once
+  std::atomic<int> rows_clusters[3][4] = {};
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mu;
@@ -944,6 +947,81 @@ int launch_gemm_epilogue(DeviceInfo *d, const PairProblem &q, int K, const Epilo
   return launch_status();
 }
 
+// Blocks of a cluster that share a 128-row tile's K in fp8_gemm_rows_kernel:
+// the most (1, 2, 4, 8) that all get a K step and whose clusters the GPU holds in
+// one go (`resident` by log2 of the cluster's size; of eight blocks, one an SM,
+// that is fewer clusters than an eighth of the SMs: 16 clusters of 8 took 9.3
+// us at N = K = 2048, their last one waiting for a place).
+int rows_split(const std::atomic<int> (&resident)[4], int64_t N, int num_kb) {
+  const int64_t tiles = (N + 127) / 128;
+  int best = 1;
+  for (int x = 1; x < 4; ++x) {
+    const int s = 1 << x, per = (num_kb + s - 1) / s;
+    if (tiles <= resident[x].load(std::memory_order_relaxed) && (s - 1) * per < num_kb) best = s;
+  }
+  return best;
+}
+
+// fp8_linear_epilogue's kernel by rows.  Up to 64 the weight streams faster
+// through fp8_gemm_rows_kernel for every N and K tried (64 rows, N x K: 10.4
+// against 12.8 us at 8192 x 2048, 7.1 against 11.8 at 2048 x 2048, 10.9 against
+// 26.2 at 2048 x 8192; 17 rows: 8.2 against 30.5, 6.0 against 13.3, 10.0
+// against 26.1).  From 65 to 128 it pays where K is split at least four ways (128 rows:
+// 10.2 against 12.1 us at 2048 x 2048, 14.4 against 26.6 at 2048 x 8192), not
+// where two ways fill the GPU (15.5 against 13.2 at 8192 x 2048) or K is short
+// (10.5 against 7.4 at 704 x 256).
+constexpr int64_t kFewLinearRows = 64;
+constexpr int64_t kFewLinearRowsSplit = 128;
+constexpr int kFewLinearSplit = 4;
+
+// *done = false: the rule above leaves this problem to the CTA-pair kernel.
+template <int NTOK, int BIT>
+int launch_gemm_rows(DeviceInfo *d, const PairProblem &q, int K, const EpilogueArgs &e,
+                     const uint16_t *residual, cudaStream_t st, bool *done) {
+  using C = RowsCfg<NTOK>;
+  auto kern = fp8_gemm_rows_kernel<NTOK>;
+  std::atomic<int>(&resident)[4] = d->rows_clusters[BIT - 42];
+  int rc = once_per_device(d, BIT, [&] {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
+        cudaSuccess)
+      return FP8WS_ERR_CUDA;
+    for (int x = 1; x < 4; ++x) {
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 1u << x;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(d->sms >> x << x);
+      cfg.blockDim = dim3(kRowsThreads);
+      cfg.dynamicSmemBytes = C::SMEM_BYTES;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int clusters = 0;
+      if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess)
+        return FP8WS_ERR_CUDA;
+      resident[x].store(clusters, std::memory_order_relaxed);
+    }
+    return FP8WS_OK;
+  });
+  if (rc) return rc;
+  const int num_kb = (K + kGemmBK - 1) / kGemmBK;
+  const int split = rows_split(resident, q.N, num_kb);
+  *done = q.M <= kFewLinearRows || split >= kFewLinearSplit;
+  if (!*done) return FP8WS_OK;
+  CUtensorMap mw, mx;
+  rc = make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.b, q.N, K, kGemmBK, 128, true);
+  if (!rc) rc = make_map_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.a, q.M, K, kGemmBK, NTOK, true);
+  if (rc) return rc;
+  const int tiles = (q.N + 127) / 128;
+  if (launch_ex(kern, dim3(tiles * split), dim3(kRowsThreads), C::SMEM_BYTES, st, split, mw, mx, e,
+                residual, q.out, q.M, q.N, K, (num_kb + split - 1) / split,
+                kWaitLimitNs) != cudaSuccess)
+    return FP8WS_ERR_CUDA;
+  log_launch(kKindGemm, q.a, q.b, q.out);
+  return launch_status();
+}
+
 // ------------------------------------------------------- 4-bit K/V cache
 // Tokens of a page as a shift; -1 unless a power of two of 16 .. 256.
 int page_shift(int page_size) {
@@ -1684,6 +1762,13 @@ int fp8_linear_epilogue(const uint8_t *xq, const uint8_t *wq, int64_t M, int64_t
   const EpilogueArgs e{s_in, s_w, bias, s_out, act};
   const int k = static_cast<int>(K);
   cudaStream_t st = as_stream(stream);
+  if (M <= kFewLinearRowsSplit) {
+    bool done = false;
+    rc = M <= 32   ? launch_gemm_rows<32, 42>(d, q, k, e, residual, st, &done)
+         : M <= 64 ? launch_gemm_rows<64, 43>(d, q, k, e, residual, st, &done)
+                   : launch_gemm_rows<128, 44>(d, q, k, e, residual, st, &done);
+    if (rc || done) return rc;
+  }
   if (s_out)
     return residual ? launch_gemm_epilogue<true, true, 36>(d, q, k, e, residual, st)
                     : launch_gemm_epilogue<true, false, 37>(d, q, k, e, nullptr, st);
