@@ -17,6 +17,7 @@ moving-average activation observer (ModelOpt W8A8, per-tensor static)"
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -791,6 +792,11 @@ def gated_mlp_per_token_fp8(x, wg, s_wg, wu, s_wu, wd, s_wd, workspace=None, out
     return out
 
 
+# The calls below are short enough on the GPU that their Python is a good part
+# of a step: shapes are unpacked once, and a tensor's checks are four attribute
+# reads unless one fails.
+
+
 def _on(first, stream):
     """(device index, raw stream) of a call on first's device."""
     if not isinstance(first, torch.Tensor):
@@ -803,14 +809,20 @@ def _on(first, stream):
     return dev, _stream(stream)
 
 
-def _ptr(t, name, dev, *dtypes):
-    """_dev_ptr for a tensor that must also be on device dev (the common case
-    is five attribute reads; the messages are _dev_ptr's)."""
-    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype in dtypes
-            and t.is_contiguous()):
-        return t.data_ptr()
-    _dev_ptr(t, name, dtypes)
+def _ptr(t, name, dev, dtype):
+    """Address of a contiguous tensor of this type on device dev."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev_ptr(t, name, (dtype,))
     raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+
+
+def _codes(t, name, dev):
+    """_ptr for FP8 codes, which may be held as bytes."""
+    return _ptr(t, name, dev, torch.uint8 if getattr(t, "dtype", None) is torch.uint8 else FP8)
 
 
 def _scalar(t, name, dev):
@@ -831,13 +843,13 @@ def _call(dev, fn, name, *args):
         raise FP8WSError(status, name)
 
 
-def _scratch(nbytes, dev, stream):
+def _scratch(nbytes, like, stream):
     """A workspace for one call on the given stream: memory of another stream
     than the current one is not handed out again before that stream is done."""
-    ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+    ws = like.new_empty(max(nbytes, 256), dtype=torch.uint8)
     if stream is not None:
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+            stream = torch.cuda.ExternalStream(int(stream), device=like.device)
         ws.record_stream(stream)
     return ws
 
@@ -854,28 +866,30 @@ def fp8_linear_epilogue(xq, wq, s_in, s_w, bias=None, act="none", residual=None,
     BF16 (residual may be out); act: "none", "relu", "silu" or "gelu" (tanh
     form)."""
     lib = load()
-    if xq.dim() != 2 or wq.dim() != 2 or xq.shape[1] != wq.shape[1]:
-        raise ValueError(f"shapes {tuple(xq.shape)} x {tuple(wq.shape)}^T do not match")
-    if act not in ACTIVATIONS:
+    a, b = xq.shape, wq.shape
+    if len(a) != 2 or len(b) != 2 or a[1] != b[1]:
+        raise ValueError(f"shapes {tuple(a)} x {tuple(b)}^T do not match")
+    kind = ACTIVATIONS.get(act)
+    if kind is None:
         raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
-    M, K = xq.shape
-    N = wq.shape[0]
-    if bias is not None and tuple(bias.shape) != (N,):
+    M, K = a
+    N = b[0]
+    if bias is not None and bias.shape != (N,):
         raise ValueError("bias must be [N]")
-    if residual is not None and tuple(residual.shape) != (M, N):
+    if residual is not None and residual.shape != (M, N):
         raise ValueError("residual must be [M, N]")
-    if out is not None and tuple(out.shape) != (M, N):
+    if out is not None and out.shape != (M, N):
         raise ValueError("out must be [M, N]")
     dev, st = _on(xq, stream)
+    bf16 = torch.bfloat16
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16 if s_out is None else FP8, device=dev)
-    bf16, u8 = torch.bfloat16, torch.uint8
-    _call(dev, lib.fp8_linear_epilogue, "fp8_linear_epilogue", _ptr(xq, "xq", dev, FP8, u8),
-          _ptr(wq, "wq", dev, FP8, u8), M, N, K, _scalar(s_in, "s_in", dev),
-          _scalar(s_w, "s_w", dev), None if bias is None else _ptr(bias, "bias", dev, bf16),
-          ACTIVATIONS[act], None if residual is None else _ptr(residual, "residual", dev, bf16),
+        out = xq.new_empty((M, N), dtype=bf16 if s_out is None else FP8)
+    _call(dev, lib.fp8_linear_epilogue, "fp8_linear_epilogue", _codes(xq, "xq", dev),
+          _codes(wq, "wq", dev), M, N, K, _scalar(s_in, "s_in", dev), _scalar(s_w, "s_w", dev),
+          None if bias is None else _ptr(bias, "bias", dev, bf16), kind,
+          None if residual is None else _ptr(residual, "residual", dev, bf16),
           None if s_out is None else _scalar(s_out, "s_out", dev),
-          _ptr(out, "out", dev, bf16) if s_out is None else _ptr(out, "out", dev, FP8, u8), st)
+          _ptr(out, "out", dev, bf16) if s_out is None else _codes(out, "out", dev), st)
     return out
 
 
@@ -884,9 +898,10 @@ def fp8_linear_epilogue(xq, wq, s_in, s_w, bias=None, act="none", residual=None,
 
 def _kv_shape(cache):
     """(pages, kv heads, page size, head dim) of a cache tensor."""
-    if not isinstance(cache, torch.Tensor) or cache.dim() != 4 or cache.shape[3] % 18:
+    shape = cache.shape
+    if len(shape) != 4 or shape[3] % 18:
         raise ValueError("cache must be [pages, kv_heads, page_size / 16, 18 * head_dim]")
-    return cache.shape[0], cache.shape[1], 16 * cache.shape[2], cache.shape[3] // 18
+    return shape[0], shape[1], 16 * shape[2], shape[3] // 18
 
 
 def fp4_kv_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int,
@@ -908,27 +923,31 @@ def fp4_kv_tables(lens, added, block_table, free_pages, used, page_size: int, n_
     out=(cu_q, kv_lens, slots, pool), where kv_lens may be lens and pool may be
     the two-element tensor given as used."""
     lib = load()
-    if lens.dim() != 1 or added.shape != lens.shape:
+    shape = lens.shape
+    if len(shape) != 1 or added.shape != shape:
         raise ValueError("lens and added must be [B]")
-    B = lens.shape[0]
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    B = shape[0]
+    table = block_table.shape
+    if len(table) != 2 or table[0] != B:
         raise ValueError("block_table must be [B, W]")
     if free_pages.dim() != 1:
         raise ValueError("free_pages must be one-dimensional")
-    if used.numel() < 1:
-        raise ValueError("used must hold one value")
     dev, st = _on(lens, stream)
     i32, i64 = torch.int32, torch.int64
     if out is None:
-        out = (torch.empty(B + 1, dtype=i32, device=dev), torch.empty(B, dtype=i32, device=dev),
-               torch.empty(n_slots, dtype=i64, device=dev), torch.empty(2, dtype=i32, device=dev))
-    cu_q, kv_lens, slots, pool = out
-    if (cu_q.numel() != B + 1 or kv_lens.numel() != B or slots.numel() != n_slots
-            or pool.numel() != 2):
-        raise ValueError("out must be cu_q [B+1], kv_lens [B], slots [n_slots] and pool [2]")
+        cu_q, kv_lens, pool = lens.new_empty(2 * B + 3, dtype=i32).split((B + 1, B, 2))
+        slots = lens.new_empty(n_slots, dtype=i64)
+        out = (cu_q, kv_lens, slots, pool)
+    else:
+        cu_q, kv_lens, slots, pool = out
+        if (cu_q.numel() != B + 1 or kv_lens.numel() != B or slots.numel() != n_slots
+                or pool.numel() != 2):
+            raise ValueError("out must be cu_q [B+1], kv_lens [B], slots [n_slots] and pool [2]")
+    if used.numel() < 1:
+        raise ValueError("used must hold one value")
     _call(dev, lib.fp4_kv_tables, "fp4_kv_tables", _ptr(lens, "lens", dev, i32),
           _ptr(added, "added", dev, i32), B, page_size, _ptr(block_table, "block_table", dev, i32),
-          block_table.shape[1], _ptr(free_pages, "free_pages", dev, i32), free_pages.numel(),
+          table[1], _ptr(free_pages, "free_pages", dev, i32), free_pages.numel(),
           _ptr(used, "used", dev, i32), _ptr(pool, "pool", dev, i32), _ptr(cu_q, "cu_q", dev, i32),
           _ptr(kv_lens, "kv_lens", dev, i32), _ptr(slots, "slots", dev, i64), n_slots, st)
     return out
@@ -940,12 +959,13 @@ def fp4_kv_append(k, v, slots, cache, s_k, s_v, stream=None) -> None:
     outside the cache is skipped, the others must differ."""
     lib = load()
     pages, heads, page, dim = _kv_shape(cache)
-    if slots.dim() != 1:
+    shape = slots.shape
+    if len(shape) != 1:
         raise ValueError("slots must be [T]")
-    T = slots.shape[0]
-    for t, n in ((k, "k"), (v, "v")):
-        if tuple(t.shape) not in ((T, heads, dim), (T, heads * dim)):
-            raise ValueError(f"{n} must be [T, {heads}, {dim}] with the T of slots")
+    T = shape[0]
+    shapes = ((T, heads, dim), (T, heads * dim))
+    if k.shape not in shapes or v.shape not in shapes:
+        raise ValueError(f"k and v must be [T, {heads}, {dim}] with the T of slots")
     dev, st = _on(cache, stream)
     _call(dev, lib.fp4_kv_append, "fp4_kv_append", _ptr(k, "k", dev, torch.bfloat16),
           _ptr(v, "v", dev, torch.bfloat16), T, heads, dim, _ptr(slots, "slots", dev, torch.int64),
@@ -958,14 +978,15 @@ def fp4_kv_gather(cache, slots, s_k, s_v, out=None, stream=None):
     the cache holds them; zeros for a slot outside the cache."""
     lib = load()
     pages, heads, page, dim = _kv_shape(cache)
-    if slots.dim() != 1:
+    shape = slots.shape
+    if len(shape) != 1:
         raise ValueError("slots must be [T]")
-    T = slots.shape[0]
+    T = shape[0]
     dev, st = _on(cache, stream)
     bf16 = torch.bfloat16
     if out is None:
-        out = (torch.empty((T, heads, dim), dtype=bf16, device=dev),
-               torch.empty((T, heads, dim), dtype=bf16, device=dev))
+        out = (cache.new_empty((T, heads, dim), dtype=bf16),
+               cache.new_empty((T, heads, dim), dtype=bf16))
     k, v = out
     if k.numel() != T * heads * dim or v.numel() != T * heads * dim:
         raise ValueError(f"out must be two tensors [T, {heads}, {dim}]")
@@ -977,6 +998,9 @@ def fp4_kv_gather(cache, slots, s_k, s_v, out=None, stream=None):
 
 def fp4_kv_attention_workspace() -> int:
     return load().fp4_kv_attention_workspace()
+
+
+_attention_workspace = functools.cache(fp4_kv_attention_workspace)  # a constant of the library
 
 
 def fp4_kv_attention(q, cu_q, kv_lens, block_table, cache, s_k, s_v, max_q: int, scale=None,
@@ -992,36 +1016,35 @@ def fp4_kv_attention(q, cu_q, kv_lens, block_table, cache, s_k, s_v, max_q: int,
     left as they were."""
     lib = load()
     pages, heads, page, dim = _kv_shape(cache)
-    if q.dim() != 3 or q.shape[2] != dim or q.shape[1] < 1 or q.shape[1] % heads:
+    shape, batch, table = q.shape, kv_lens.shape, block_table.shape
+    if len(shape) != 3 or shape[2] != dim or shape[1] < 1 or heads < 1 or shape[1] % heads:
         raise ValueError(f"q must be [total_q, a multiple of {heads}, {dim}]")
-    if kv_lens.dim() != 1 or tuple(cu_q.shape) != (kv_lens.shape[0] + 1,):
+    if len(batch) != 1 or cu_q.shape != (batch[0] + 1,):
         raise ValueError("kv_lens must be [B] and cu_q [B + 1]")
-    B = kv_lens.shape[0]
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    B = batch[0]
+    if len(table) != 2 or table[0] != B:
         raise ValueError("block_table must be [B, W]")
-    if scale is None:
-        scale = dim ** -0.5
-    if out is not None and out.shape != q.shape:
+    if out is not None and out.shape != shape:
         raise ValueError("out must have q's shape")
-    if lse is not None and lse.shape != q.shape[:2]:
+    if lse is not None and lse.shape != shape[:2]:
         raise ValueError("lse must be [total_q, q_heads]")
     dev, st = _on(q, stream)
+    bf16, f32, i32, u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
     if workspace is None:
-        workspace = _scratch(lib.fp4_kv_attention_workspace(), dev, stream)
-    bf16, i32, u8 = torch.bfloat16, torch.int32, torch.uint8
+        workspace = _scratch(_attention_workspace(), q, stream)
     if out is None:
-        out = torch.empty(q.shape, dtype=bf16 if s_out is None else FP8, device=dev)
+        out = q.new_empty(shape, dtype=bf16 if s_out is None else FP8)
     if return_lse and lse is None:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
-    _call(dev, lib.fp4_kv_attention, "fp4_kv_attention", _ptr(q, "q", dev, bf16), q.shape[0],
-          q.shape[1], B, _ptr(cu_q, "cu_q", dev, i32), _ptr(kv_lens, "kv_lens", dev, i32), max_q,
-          _ptr(block_table, "block_table", dev, i32), block_table.shape[1],
-          _ptr(cache, "cache", dev, u8), pages, page, heads, dim, _scalar(s_k, "s_k", dev),
-          _scalar(s_v, "s_v", dev), float(scale), int(bool(causal)),
+        lse = q.new_empty(shape[:2], dtype=f32)
+    _call(dev, lib.fp4_kv_attention, "fp4_kv_attention", _ptr(q, "q", dev, bf16), shape[0],
+          shape[1], B, _ptr(cu_q, "cu_q", dev, i32), _ptr(kv_lens, "kv_lens", dev, i32), max_q,
+          _ptr(block_table, "block_table", dev, i32), table[1], _ptr(cache, "cache", dev, u8),
+          pages, page, heads, dim, _scalar(s_k, "s_k", dev), _scalar(s_v, "s_v", dev),
+          dim ** -0.5 if scale is None else scale, 1 if causal else 0,
           None if s_out is None else _scalar(s_out, "s_out", dev),
-          _ptr(out, "out", dev, bf16) if s_out is None else _ptr(out, "out", dev, FP8, u8),
-          None if lse is None else _ptr(lse, "lse", dev, torch.float32),
-          _ptr(workspace, "workspace", dev, u8), workspace.numel(), st)
+          _ptr(out, "out", dev, bf16) if s_out is None else _codes(out, "out", dev),
+          None if lse is None else _ptr(lse, "lse", dev, f32), _ptr(workspace, "workspace", dev, u8),
+          workspace.numel(), st)
     return (out, lse) if return_lse else out
 
 
