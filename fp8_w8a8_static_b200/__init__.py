@@ -935,7 +935,7 @@ def fp4_kv_tables(lens, added, block_table, free_pages, used, page_size: int, n_
     dev, st = _on(lens, stream)
     i32, i64 = torch.int32, torch.int64
     if out is None:
-        cu_q, kv_lens, pool = lens.new_empty(2 * B + 3, dtype=i32).split((B + 1, B, 2))
+        cu_q, kv_lens, pool = lens.new_empty(B + 1), lens.new_empty(B), lens.new_empty(2)
         slots = lens.new_empty(n_slots, dtype=i64)
         out = (cu_q, kv_lens, slots, pool)
     else:

@@ -4,18 +4,25 @@
 // The operation, the cache and the row packing are those of fp4_attention.cuh.
 // A block takes 256 rows (two 128-row tiles) of one request and K/V head and
 // walks the tokens that any of them sees, 128 at a time:
-//   warp 0        copies strips into a two-slot ring (bulk copies, one a strip)
+//   warp 0        copies strips into a ring, four (64 tokens) a slot
 //   warps 12..15  turn codes into FP16 once for both row tiles: K and V as
 //                 [token][64 elements] 128-byte-swizzled atoms.  K is read
 //                 K-major, V MN-major (its inner index, the token, is the row),
 //                 so both are written the same way and nothing is transposed.
-//   warp 1        issues the MMAs: S_t = Q_t K^T (M = 128, N = 128) into TMEM,
+//   warp 1        issues the MMAs: S = Q_t K^T (M = 128, N = 128) into TMEM,
 //                 O_t += P_t V with P_t read from TMEM
 //   warps 4..11   softmax: four warps a row tile, a thread a row, so the maximum
-//                 and the sum need no exchange.  P (FP16) takes the place of S.
-// The two row tiles alternate: one's products run while the other's weights are
-// computed.  A row's maximum is moved, and its sums in TMEM scaled, only when a
-// score exceeds it by 2^10 (FP16 weights have that room).
+//                 and the sum need no exchange.
+// The row tiles alternate: one's products run while the other's weights are
+// computed.  A score tile is read twice from TMEM, for the maximum and for the
+// weights (its 128 values a thread do not fit in registers beside the rest, even
+// with 200 a thread; a read costs 50 cycles a 64 columns).  With D = 64 there is
+// room for P beside S, and the next scores are computed during the exponentials;
+// with D = 128 P takes S's place.  (One S for both row tiles and P apart, the
+// other way to 512 columns, was slower: 375 against 350 us for 2 chunks of 2048
+// rows.)  A row's
+// maximum is moved, and its sums in TMEM scaled, only when a score exceeds it
+// by 2^10 (FP16 weights have that room).
 // Bound: 128 x 128 scores are 1024 cycles of the tensor pipe (D = 128: two
 // products of 512) and 1024 of the special function unit (one exponential
 // each, 16 a cycle), side by side; the codes' conversion is 256 cycles of the
@@ -32,17 +39,23 @@ constexpr int kKvTileTokens = 128;
 constexpr int kKvTileStrips = kKvTileTokens / kStripTokens;
 constexpr int kKvTileThreads = 512;
 constexpr int kKvMasks = 8;  // tiles whose missing strips are remembered
+constexpr int kKvRawSlots = 3;    // ring of raw strips
+constexpr int kKvRawStrips = 4;   // strips of a slot
 
 template <int D>
 struct KvTilesCfg {
   static constexpr int ATOMS = D / 64;                 // 64-element atoms of a row
   static constexpr int ATOM = 128 * 128;               // 128 rows of 128 bytes
   static constexpr int TILE = ATOMS * ATOM;            // Q, K or V of 128 rows, FP16
-  static constexpr int RAW = kKvTileStrips * strip_bytes(D);
-  static constexpr int RAW_PAD = (RAW + 1023) / 1024 * 1024;
-  // two tiles of Q, one of K, two of V, two of raw strips
-  static constexpr int SMEM = 5 * TILE + 2 * RAW_PAD + 1024;
-  static constexpr int O_COL = 256;  // TMEM columns: S/P of both tiles, then O of both
+  static constexpr int RAW = kKvRawStrips * strip_bytes(D);
+  // two tiles each of Q, K and V, the ring of raw strips
+  static constexpr int SMEM = 6 * TILE + kKvRawSlots * RAW + 1024;
+  // TMEM columns: S of both row tiles (128 each), O of both, then P of both (two
+  // FP16 a column) where there is room (D = 64); else P takes S's place
+  static constexpr bool P_APART = D == 64;
+  static constexpr int O_COL = 256;
+  static constexpr int P_COL = P_APART ? 256 + 2 * D : 0;
+  static constexpr int P_STEP = P_APART ? 64 : 128;
   static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -52,40 +65,42 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_maj
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// MN-major operand in 128-byte-swizzled atoms of 64 elements (128 bytes) by 8
-// inner rows: 8-row groups 1024 bytes apart (stride), 64-element blocks `block`
-// bytes apart (leading).
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t block) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>((block >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
+// Operand descriptors in two words.  The issuing thread shares its scheduler
+// with softmax and conversion warps, so an MMA has to cost it few instructions:
+// the high word is a constant, and of the low one only the start address
+// (>> 4, the low 14 bits) moves, by a constant from one MMA to the next.  (With
+// 64-bit descriptors put together for each MMA its issue took 160 cycles, the
+// MMA itself 65.)
+//   high word: 8-row groups 1024 bytes apart, version 1, 128-byte swizzle
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+// K-major: rows of 128 bytes (64 elements of the inner index).
+__device__ __forceinline__ uint32_t desc_k_major(uint32_t saddr) { return saddr >> 4 | 1u << 16; }
+// MN-major: rows are the inner index, 64 elements each; the next 64 elements
+// lie `block` bytes on.
+__device__ __forceinline__ uint32_t desc_mn_major(uint32_t saddr, uint32_t block) {
+  return saddr >> 4 | block >> 4 << 16;
 }
 
-__device__ __forceinline__ void umma_f16_ss(uint32_t tmem_d, uint64_t desc_a, uint64_t desc_b,
-                                            uint32_t idesc, uint32_t accumulate) {
-  uint32_t z = 0;  // no output lane disabled
+template <bool ACC>
+__device__ __forceinline__ void umma_f16_ss(uint32_t tmem_d, uint32_t a_low, uint32_t b_low,
+                                            uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}" ::"r"(
-          tmem_d),
-      "l"(desc_a), "l"(desc_b), "r"(idesc), "r"(accumulate), "r"(z));
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(a_low), "r"(b_low), "r"(idesc), "n"(kDescHigh), "n"(ACC ? 1 : 0));
 }
 
 // A from TMEM: lane = row, a column holds two neighbouring elements.
-__device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t desc_b,
+__device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_low,
                                             uint32_t idesc, uint32_t accumulate) {
-  uint32_t z = 0;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %5, %5, %5}, p;\n\t}" ::"r"(
-          tmem_d),
-      "r"(tmem_a), "l"(desc_b), "r"(idesc), "r"(accumulate), "r"(z));
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %4};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "r"(b_low), "r"(idesc), "n"(kDescHigh), "r"(accumulate));
 }
 
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -97,18 +112,14 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31])
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 
 __device__ __forceinline__ void tmem_st_wait() {
@@ -131,12 +142,13 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t *sQ = smem;                // [2] tiles
-  uint8_t *sK = smem + 2 * C::TILE;
-  uint8_t *sV = sK + C::TILE;        // [2]
-  uint8_t *sRaw = sV + 2 * C::TILE;  // [2]
-  __shared__ __align__(8) uint64_t raw_full[2], raw_empty[2], k_full, k_empty, v_full[2],
-      v_empty[2], s_full[2], p_full[2], pv_done[2], drain;
+  uint8_t *sQ = smem;                // [2] tiles each
+  uint8_t *sK = sQ + 2 * C::TILE;
+  uint8_t *sV = sK + 2 * C::TILE;
+  uint8_t *sRaw = sV + 2 * C::TILE;  // [kKvRawSlots]
+  // [2]: by buffer (K, V) or by row tile (S, P, O)
+  __shared__ __align__(8) uint64_t raw_full[kKvRawSlots], raw_empty[kKvRawSlots], k_full[2],
+      k_empty[2], v_full[2], v_empty[2], s_full[2], s_read[2], p_full[2][2], pv_done[2], drain;
   __shared__ uint32_t missing[kKvMasks];  // strips that the cache lacks, a bit each
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
@@ -145,17 +157,21 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kKvRawSlots; ++s) {
       mbar_init(&raw_full[s], 1);
       mbar_init(&raw_empty[s], 4);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&k_full[s], 4);
+      mbar_init(&k_empty[s], 1);
       mbar_init(&v_full[s], 4);
       mbar_init(&v_empty[s], 1);
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 4);
+      mbar_init(&s_read[s], 4);
+      mbar_init(&p_full[s][0], 4);
+      mbar_init(&p_full[s][1], 4);
       mbar_init(&pv_done[s], 1);
     }
-    mbar_init(&k_full, 4);
-    mbar_init(&k_empty, 1);
     mbar_init(&drain, 1);
     abort_word = 0;
     fence_mbar_init();
@@ -214,31 +230,39 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
   const int most = kv_limit(req, (row0 + rows - 1) / a.group, a.causal);
   const int tiles = (most + kKvTileTokens - 1) / kKvTileTokens;
 
+  // A wait of the whole warp, and what follows when it runs out.
+  auto wait = [&](uint64_t *bar, int n) {
+    if (mbar_wait_polled_warp(bar, n & 1, abort_flag, timeout_ns)) return true;
+    if (lane == 0) {
+      record_timeout(kSiteKvTiles);
+      *abort_flag = 1;
+    }
+    return false;
+  };
+
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     const int32_t *table = a.table + static_cast<int64_t>(b) * a.width;
     const int strips = (most + kStripTokens - 1) / kStripTokens;
+    const int slots = (strips + kKvRawStrips - 1) / kKvRawStrips;
     auto page_of = [&](int strip) {
-      return lane < kKvTileStrips && strip < strips
+      return lane < kKvRawStrips && strip < strips
                  ? table[(strip * kStripTokens) >> a.cache.page_shift]
                  : -1;
     };
     int page = page_of(lane);
-    int j = 0;
-    for (; j < tiles; ++j) {
-      const int slot = j & 1;
-      if (!mbar_wait_polled_warp(&raw_empty[slot], (j >> 1 & 1) ^ 1, abort_flag, timeout_ns)) {
-        if (lane == 0) {
-          record_timeout(kSiteKvTiles);
-          *abort_flag = 1;
-        }
-        break;
-      }
-      const int strip = j * kKvTileStrips + lane;
+    int i = 0;
+    for (; i < slots; ++i) {
+      const int slot = i % kKvRawSlots;
+      if (!wait(&raw_empty[slot], i / kKvRawSlots + 1)) break;
+      const int strip = i * kKvRawStrips + lane;
       const bool there = page >= 0 && page < a.cache.pages;
       const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there);
       if (lane == 0) {
-        missing[j % kKvMasks] = ~mask & ((1u << kKvTileStrips) - 1);
+        // (the strips of the tile's second half are missing until told otherwise)
+        const uint32_t gone = ~mask & ((1u << kKvRawStrips) - 1);
+        uint32_t *word = &missing[i / 2 % kKvMasks];
+        *word = i & 1 ? (*word & 0x0Fu) | gone << kKvRawStrips : 0xF0u | gone;
         mbar_arrive_expect_tx(&raw_full[slot], __popc(mask) * strip_bytes(D));
       }
       __syncwarp();
@@ -246,16 +270,16 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
         const int64_t at = ((static_cast<int64_t>(page) * a.cache.heads + head)
                             << (a.cache.page_shift - 4)) +
                            (strip & ((1 << (a.cache.page_shift - 4)) - 1));
-        bulk_load_1d(sRaw + slot * C::RAW_PAD + lane * strip_bytes(D),
+        bulk_load_1d(sRaw + slot * C::RAW + lane * strip_bytes(D),
                      a.cache.data + at * strip_bytes(D), strip_bytes(D), &raw_full[slot],
                      l2_policy_evict_normal());
       }
-      page = page_of(strip + kKvTileStrips);
+      page = page_of(strip + kKvRawStrips);
     }
-    if (j < tiles) {  // copies in flight land before the block may end
+    if (i < slots) {  // copies in flight land before the block may end
       int zero = 0;
-      for (int k = max(j - 2, 0); k < j; ++k)
-        mbar_wait_polled_warp(&raw_full[k & 1], k >> 1 & 1, &zero, timeout_ns);
+      for (int k = max(i - kKvRawSlots, 0); k < i; ++k)
+        mbar_wait_polled_warp(&raw_full[k % kKvRawSlots], k / kKvRawSlots & 1, &zero, timeout_ns);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issue
@@ -263,9 +287,8 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
     if (lane == 0 && tiles > 0) {
       constexpr uint32_t idesc_s = idesc_f16_f32(128, kKvTileTokens, false);
       constexpr uint32_t idesc_o = idesc_f16_f32(128, D, true);
-      // every barrier below completes once a tile
-      auto wait = [&](uint64_t *bar, int n) -> bool {
-        if (mbar_wait_bounded(bar, n & 1, abort_flag, timeout_ns)) {
+      auto wait1 = [&](uint64_t *bar, int n) -> bool {
+        if (mbar_wait_polled(bar, n & 1, abort_flag, timeout_ns)) {
           tc_fence_after();
           return true;
         }
@@ -273,44 +296,56 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
         *abort_flag = 1;
         return false;
       };
-      auto scores = [&](int t) {  // S_t = Q_t K^T
-        const uint32_t q = smem_u32(sQ + t * C::TILE), k = smem_u32(sK);
+      const uint32_t q_desc = desc_k_major(smem_u32(sQ)), k_desc = desc_k_major(smem_u32(sK));
+      const uint32_t v_desc = desc_mn_major(smem_u32(sV), C::ATOM);
+      // step n is row tile n % row_tiles at token tile n / row_tiles
+      const int steps = tiles * row_tiles;
+      auto scores = [&](int n) -> bool {  // S = Q_t K^T
+        const int t = n % row_tiles, j = n / row_tiles;
+        if (t == 0 && !wait1(&k_full[j & 1], j >> 1)) return false;
+        const uint32_t q = q_desc + t * (C::TILE >> 4), k = k_desc + (j & 1) * (C::TILE >> 4);
+        const uint32_t d = tmem + t * kKvTileTokens;
+        umma_f16_ss<false>(d, q, k, idesc_s);
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          const uint32_t at = x / 4 * C::ATOM + x % 4 * 32;
-          umma_f16_ss(tmem + t * kKvTileTokens, smem_desc_k_sw128(q + at),
-                      smem_desc_k_sw128(k + at), idesc_s, x != 0);
+        for (int x = 1; x < D / 16; ++x) {
+          const uint32_t at = (x / 4 * C::ATOM + x % 4 * 32) >> 4;
+          umma_f16_ss<true>(d, q + at, k + at, idesc_s);
         }
         umma_commit(&s_full[t]);
+        if (t == row_tiles - 1) umma_commit(&k_empty[j & 1]);
+        return true;
       };
-      auto sums = [&](int t, int j) {  // O_t += P_t V
-        const uint32_t v = smem_u32(sV + (j & 1) * C::TILE);
+      auto sums = [&](int n) -> bool {  // O_t += P_t V, P in two halves
+        const int t = n % row_tiles, j = n / row_tiles;
+        if (t == 0 && !wait1(&v_full[j & 1], j >> 1)) return false;
+        const uint32_t v = v_desc + (j & 1) * (C::TILE >> 4);
+        const uint32_t d = tmem + C::O_COL + t * D, p = tmem + C::P_COL + t * C::P_STEP;
 #pragma unroll
-        for (int x = 0; x < kKvTileTokens / 16; ++x)
-          umma_f16_ts(tmem + C::O_COL + t * 128, tmem + t * kKvTileTokens + x * 8,
-                      smem_desc_mn_sw128(v + x * 2048, C::ATOM), idesc_o, (j | x) != 0);
+        for (int h = 0; h < 2; ++h) {
+          if (!wait1(&p_full[t][h], j)) return false;
+#pragma unroll
+          for (int x = 0; x < kKvTileTokens / 32; ++x) {
+            const int k = h * (kKvTileTokens / 32) + x;
+            umma_f16_ts(d, p + k * 8, v + k * (2048 >> 4), idesc_o, k != 0 || j != 0);
+          }
+        }
         umma_commit(&pv_done[t]);
+        if (t == row_tiles - 1) umma_commit(&v_empty[j & 1]);
+        return true;
       };
-      bool ok = wait(&k_full, 0);
-      if (ok) {
-        for (int t = 0; t < row_tiles; ++t) scores(t);
-        umma_commit(&k_empty);
-      }
-      for (int j = 0; j < tiles && ok; ++j) {
-        ok = wait(&v_full[j & 1], j >> 1);
-        const bool more = j + 1 < tiles;
-        for (int t = 0; t < row_tiles && ok; ++t) {
-          ok = wait(&p_full[t], j);
-          if (!ok) break;
-          sums(t, j);
-          if (t == row_tiles - 1) umma_commit(&v_empty[j & 1]);
-          if (!more) continue;
-          if (t == 0) ok = wait(&k_full, j + 1);
-          // P_t lies where S_t goes
-          if (ok) ok = wait(&pv_done[t], j);
-          if (!ok) break;
-          scores(t);
-          if (t == row_tiles - 1) umma_commit(&k_empty);
+      bool ok = true;
+      for (int n = 0; n < row_tiles && ok; ++n) ok = scores(n);
+      for (int n = 0; n < steps && ok; ++n) {
+        const int t = n % row_tiles, j = n / row_tiles;
+        const bool more = n + row_tiles < steps;
+        if constexpr (C::P_APART) {
+          // the next scores as soon as these are in registers
+          if (more) ok = wait1(&s_read[t], j) && scores(n + row_tiles);
+          if (ok) ok = sums(n);
+        } else {
+          ok = sums(n);
+          // P lies where the next scores go
+          if (ok && more) ok = wait1(&pv_done[t], j) && scores(n + row_tiles);
         }
       }
       umma_commit(&drain);
@@ -322,30 +357,22 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
     // ------------------------------------------------------------ codes to FP16
     const int w = warp - 12;
     bool ok = true;
-    auto wait = [&](uint64_t *bar, int n) {
-      if (mbar_wait_polled_warp(bar, n & 1, abort_flag, timeout_ns)) return true;
-      if (lane == 0) {
-        record_timeout(kSiteKvTiles);
-        *abort_flag = 1;
-      }
-      return false;
-    };
-    // this warp's two strips (32 tokens) of K or V
-    auto convert = [&](const uint8_t *raw, uint8_t *tile, bool is_v, int tok0, uint32_t gone) {
+    // this warp's strip of a slot: 16 tokens of K or V; row0 of the 128-token tile
+    auto convert = [&](const uint8_t *strip, uint8_t *tile, bool is_v, int row0, int tok0,
+                       bool gone) {
       constexpr int LANES = D / 32;      // lanes of a row, 32 elements (16 bytes of codes) each
       constexpr int ROWS = 32 / LANES;   // rows of a round
       const int part = lane % LANES;
-#pragma unroll
-      for (int x = 0; x < 32 / ROWS; ++x) {
-        const int row = w * 32 + x * ROWS + lane / LANES;  // in the tile
-        const int in = row % kStripTokens;
-        const uint8_t *strip = raw + row / kStripTokens * strip_bytes(D);
+#pragma unroll 1
+      for (int x = 0; x < kStripTokens / ROWS; ++x) {
+        const int in = x * ROWS + lane / LANES;
+        const int row = row0 + in;
         const uint4 codes = *reinterpret_cast<const uint4 *>(strip + (is_v ? strip_v(D) : 0) +
                                                              in * (D / 2) + part * 16);
         uint32_t sc = *reinterpret_cast<const uint16_t *>(
             strip + (is_v ? strip_vs(D) : strip_ks(D)) + in * (D / 16) + part * 2);
         // V of tokens that are not there has to be finite: rows weigh it with 0
-        if (is_v && (tok0 + row >= req.kv || (gone >> (row / kStripTokens) & 1u))) sc = 0;
+        if (is_v && (gone || tok0 + row >= req.kv)) sc = 0;
         const uint32_t sh = cvt_f16_e4m3x2(sc);
         const __half2 s = *reinterpret_cast<const __half2 *>(&sh);
         const __half2 s0 = __low2half2(s), s1 = __high2half2(s);
@@ -373,27 +400,38 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
         }
       }
     };
+    const int slots = (most + kKvRawStrips * kStripTokens - 1) / (kKvRawStrips * kStripTokens);
     for (int j = 0; j < tiles && ok; ++j) {
-      const int slot = j & 1;
-      const uint8_t *raw = sRaw + slot * C::RAW_PAD;
-      const int tok0 = j * kKvTileTokens;
-      ok = wait(&raw_full[slot], j >> 1);
-      if (!ok) break;
-      const uint32_t gone = missing[j % kKvMasks];
-      ok = wait(&k_empty, j + 1);  // the products with the K before are done
-      if (!ok) break;
-      convert(raw, sK, false, tok0, gone);
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&k_full);
-      ok = wait(&v_empty[slot], (j >> 1) + 1);
-      if (!ok) break;
-      convert(raw, sV + slot * C::TILE, true, tok0, gone);
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&v_full[slot]);
-        mbar_arrive(&raw_empty[slot]);
+      const int buf = j & 1, tok0 = j * kKvTileTokens;
+      uint8_t *k_tile = sK + buf * C::TILE, *v_tile = sV + buf * C::TILE;
+      // the products with the K and V two tiles before are done
+      ok = wait(&k_empty[buf], (j >> 1) + 1);
+      for (int h = 0; h < 2 && ok; ++h) {
+        const int i = 2 * j + h, slot = i % kKvRawSlots;
+        const int row0 = (h * kKvRawStrips + w) * kStripTokens;
+        const uint8_t *strip = sRaw + slot * C::RAW + w * strip_bytes(D);
+        bool gone = true;  // the last tile may lack its second slot
+        if (i < slots) {
+          ok = wait(&raw_full[slot], i / kKvRawSlots);
+          if (!ok) break;
+          gone = missing[j % kKvMasks] >> (h * kKvRawStrips + w) & 1u;
+          convert(strip, k_tile, false, row0, tok0, gone);
+        }
+        if (h == 1) {
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&k_full[buf]);
+        }
+        if (h == 0) ok = wait(&v_empty[buf], (j >> 1) + 1);
+        if (!ok) break;
+        convert(strip, v_tile, true, row0, tok0, gone);
+        if (h == 1) {
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&v_full[buf]);
+        }
+        __syncwarp();
+        if (i < slots && lane == 0) mbar_arrive(&raw_empty[slot]);
       }
     }
   } else if (warp >= 4) {
@@ -419,7 +457,8 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
         for (int y = 0; y < 4; ++y) top = max(top, max(w[y] & 0x7FFFu, (w[y] >> 16) & 0x7FFFu));
       }
       const int e = top == 0 ? 0 : min(max(static_cast<int>(top >> 7) - 127, -126), 126);
-      c = fabsf(factor) * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      // (not 0 either: -inf, a score not seen, stays -inf)
+      c = fmaxf(fabsf(factor) * __uint_as_float(static_cast<uint32_t>(127 + e) << 23), 0x1p-126f);
       const float down =
           copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), factor);
       uint8_t *to = sQ + tile * C::TILE + (quarter * 32 + lane) * 128;
@@ -437,97 +476,108 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
     const bool used = tile < row_tiles;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t t_s = tmem + lanes + tile * kKvTileTokens;
-    const uint32_t t_o = tmem + lanes + C::O_COL + tile * 128;
+    const uint32_t t_p = tmem + lanes + C::P_COL + tile * C::P_STEP;
+    const uint32_t t_o = tmem + lanes + C::O_COL + tile * D;
     float neg_m = INFINITY, l = 0.0f;  // minus the maximum in log2 units, the sum
     bool ok = true;
-    auto wait = [&](uint64_t *bar, int n) {
-      if (mbar_wait_polled_warp(bar, n & 1, abort_flag, timeout_ns)) return true;
-      if (lane == 0) {
-        record_timeout(kSiteKvTiles);
-        *abort_flag = 1;
-      }
-      return false;
-    };
     for (int j = 0; used && j < tiles; ++j) {
       ok = wait(&s_full[tile], j);
       if (!ok) break;
       tc_fence_after();
       const int tok0 = j * kKvTileTokens;
       const uint32_t gone = missing[j % kKvMasks];
-      const bool edge =
-          __any_sync(0xFFFFFFFFu, tok0 + kKvTileTokens > lim) || gone != 0;
-      // a score that the row does not see is -inf
-      auto masked = [&](uint32_t (&s)[32], int col) {
+      const bool edge = __any_sync(0xFFFFFFFFu, tok0 + kKvTileTokens > lim) || gone != 0;
+      uint32_t s0[32], s1[32];  // scores of two 32-token chunks
+      // of an edge tile: a score that the row does not see is -inf
+      auto mask = [&](uint32_t (&s)[32], int tok, uint32_t gone) {
+        const int n0 = gone & 1u ? 0 : lim - tok, n1 = gone & 2u ? 0 : lim - tok;
 #pragma unroll
         for (int x = 0; x < 32; ++x)
-          if (tok0 + col + x >= lim || (gone >> ((col + x) / kStripTokens) & 1u))
-            s[x] = 0xFF800000u;
+          if (x >= (x < kStripTokens ? n0 : n1)) s[x] = 0xFF800000u;
+      };
+      auto largest = [&](const uint32_t (&s)[32], float top) {
+        float other = top;
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) {
+          top = fmaxf(top, __uint_as_float(s[x]));
+          other = fmaxf(other, __uint_as_float(s[x + 1]));
+        }
+        return fmaxf(top, other);
+      };
+      auto load = [&](int h) {  // the scores of 64 tokens
+        tmem_ld_32x32b_x32(t_s + h * 64, s0);
+        tmem_ld_32x32b_x32(t_s + h * 64 + 32, s1);
+        tmem_ld_wait();
+        if (edge) {
+          mask(s0, tok0 + h * 64, gone >> (4 * h));
+          mask(s1, tok0 + h * 64 + 32, gone >> (4 * h + 2));
+        }
       };
       float top = -INFINITY;
-#pragma unroll
-      for (int col = 0; col < kKvTileTokens; col += 32) {
-        uint32_t s[32];
-        tmem_ld_32x32b_x32(t_s + col, s);
-        tmem_ld_wait();
-        if (edge) masked(s, col);
-#pragma unroll
-        for (int x = 0; x < 32; ++x) top = fmaxf(top, __uint_as_float(s[x]));
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        load(h);
+        top = largest(s1, largest(s0, top));
       }
       const float now = top == -INFINITY ? -INFINITY : top * c;
-      if (__any_sync(0xFFFFFFFFu, now + neg_m > kKvSlack)) {
-        // move the maxima (at first from -inf); O must not be in use
+      // P's columns, where they are not S's, and O's, where they are to be scaled,
+      // are in use until the last products are done
+      const bool move = __any_sync(0xFFFFFFFFu, now + neg_m > kKvSlack);
+      if (j > 0 && (move || C::P_APART)) {
+        ok = wait(&pv_done[tile], j - 1);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      if (move) {
+        // move the maxima (at first from -inf)
         const float next = fmaxf(-neg_m, now);
         const float by = next == -INFINITY ? 1.0f : ex2_approx(-neg_m - next);
         neg_m = next == -INFINITY ? INFINITY : -next;
         l *= by;
         if (j > 0) {
-          ok = wait(&pv_done[tile], j - 1);
-          if (!ok) break;
-          tc_fence_after();
 #pragma unroll 1
-          for (int col = 0; col < D; col += 32) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(t_o + col, o);
+          for (int col = 0; col < D; col += 16) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(t_o + col, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * by);
-            tmem_st_32x32b_x32(t_o + col, o);
+            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * by);
+            tmem_st_32x32b_x16(t_o + col, o);
           }
         }
       }
-      // weights; chunk by chunk P takes the columns of scores already read
+      // a row that has seen nothing yet has no maximum: any, for weights of 0
+      const float shift = neg_m == INFINITY ? 0.0f : neg_m;
+      float sums[2] = {0.0f, 0.0f};
+      // weights of a chunk, rounded to FP16 (2^-11 of each) for the second product
+      auto weigh = [&](const uint32_t (&s)[32], uint32_t col) {
+        uint32_t p[16];
 #pragma unroll
-      for (int col = 0; col < kKvTileTokens; col += 32) {
-        uint32_t s[32], p[16];
-        tmem_ld_32x32b_x32(t_s + col, s);
-        tmem_ld_wait();
-        float part[2] = {0.0f, 0.0f};
-        if (edge) {
-          masked(s, col);
-#pragma unroll
-          for (int x = 0; x < 32; ++x) {
-            const bool unseen = s[x] == 0xFF800000u;
-            s[x] = unseen ? 0u
-                          : __float_as_uint(ex2_approx(fmaf(__uint_as_float(s[x]), c, neg_m)));
-          }
-        } else {
-#pragma unroll
-          for (int x = 0; x < 32; ++x)
-            s[x] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(s[x]), c, neg_m)));
+        for (int x = 0; x < 16; ++x) {
+          const float e0 = ex2_approx(fmaf(__uint_as_float(s[2 * x]), c, shift));
+          const float e1 = ex2_approx(fmaf(__uint_as_float(s[2 * x + 1]), c, shift));
+          sums[0] += e0;
+          sums[1] += e1;
+          p[x] = pack_f16(e0, e1);
         }
-#pragma unroll
-        for (int x = 0; x < 32; ++x) part[x & 1] += __uint_as_float(s[x]);
-        l += part[0] + part[1];
-        // P is rounded to FP16 (2^-11 of each weight) for the second product
-#pragma unroll
-        for (int x = 0; x < 16; ++x)
-          p[x] = pack_f16(__uint_as_float(s[2 * x]), __uint_as_float(s[2 * x + 1]));
-        tmem_st_32x32b_x16(t_s + col / 2, p);
+        tmem_st_32x32b_x16(col, p);
+      };
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        load(h);
+        if (C::P_APART && h == 1) {  // the columns may take the next scores
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_read[tile]);
+        }
+        weigh(s0, t_p + h * 32);
+        weigh(s1, t_p + h * 32 + 16);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[tile][h]);  // 64 tokens' weights are there
       }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[tile]);
+      l += sums[0] + sums[1];
     }
     if (used && ok && tiles > 0) {
       ok = wait(&pv_done[tile], tiles - 1);
