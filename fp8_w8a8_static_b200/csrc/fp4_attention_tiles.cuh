@@ -3,30 +3,29 @@
 //
 // The operation, the cache and the row packing are those of fp4_attention.cuh.
 // A block takes 256 rows (two 128-row tiles) of one request and K/V head and
-// walks the tokens that any of them sees, 128 at a time:
-//   warp 0        copies strips into a ring, four (64 tokens) a slot
+// walks the tokens that any of them sees, 64 (a chunk) at a time:
+//   warp 0        copies the chunk's strips into a ring
 //   warps 12..15  turn codes into FP16 once for both row tiles: K and V as
-//                 [token][64 elements] 128-byte-swizzled atoms.  K is read
-//                 K-major, V MN-major (its inner index, the token, is the row),
-//                 so both are written the same way and nothing is transposed.
-//   warp 1        issues the MMAs: S = Q_t K^T (M = 128, N = 128) into TMEM,
-//                 O_t += P_t V with P_t read from TMEM
+//                 [token][64 elements] 128-byte-swizzled atoms, four chunks
+//                 deep.  K is read K-major, V MN-major (its inner index, the
+//                 token, is the row), so both are written the same way and
+//                 nothing is transposed.
+//   warp 1        issues the MMAs: S = Q_t K^T (M = 128, N = 64) into TMEM,
+//                 O_t += P_t V with P_t read from TMEM, in S's place
 //   warps 4..11   softmax: four warps a row tile, a thread a row, so the maximum
-//                 and the sum need no exchange.
-// The row tiles alternate: one's products run while the other's weights are
-// computed.  A score tile is read twice from TMEM, for the maximum and for the
-// weights (its 128 values a thread do not fit in registers beside the rest, even
-// with 200 a thread; a read costs 50 cycles a 64 columns).  With D = 64 there is
-// room for P beside S, and the next scores are computed during the exponentials;
-// with D = 128 P takes S's place.  (One S for both row tiles and P apart, the
-// other way to 512 columns, was slower: 375 against 350 us for 2 chunks of 2048
-// rows.)  A row's
-// maximum is moved, and its sums in TMEM scaled, only when a score exceeds it
-// by 2^10 (FP16 weights have that room).
-// Bound: 128 x 128 scores are 1024 cycles of the tensor pipe (D = 128: two
-// products of 512) and 1024 of the special function unit (one exponential
-// each, 16 a cycle), side by side; the codes' conversion is 256 cycles of the
-// conversion unit for 256 rows.
+//                 and the sum need no exchange; a chunk's scores stay in
+//                 registers from the search for the maximum to the weights.
+// Each row tile has two score buffers: while the softmax is on one chunk, the
+// next one's scores are computed, and a chunk's scores are asked for one event
+// after the products that free their buffer, when the other row tile's are in
+// between, so that the issuing thread hardly waits.  (Chunks of 128 tokens with
+// one buffer a row tile, products and scores taking turns: 315 against 240 us
+// for 2 chunks of 2048 rows, and 280 with the softmax left out.)  A row's maximum
+// is moved, and its sums in TMEM scaled, only when a score exceeds it by 2^10
+// (FP16 weights have that room).
+// Bound, for 256 rows and 64 tokens: 2 x (390 + 260) cycles of the tensor pipe
+// (D = 128; the first product, N = 64, is held by the reads of Q) beside 1024 of
+// the special function unit (one exponential a score, 16 a cycle).
 #pragma once
 
 #include "common.cuh"
@@ -35,27 +34,22 @@
 namespace fp8ws {
 
 constexpr int kKvTileRows = 256;
-constexpr int kKvTileTokens = 128;
-constexpr int kKvTileStrips = kKvTileTokens / kStripTokens;
 constexpr int kKvTileThreads = 512;
-constexpr int kKvMasks = 8;  // tiles whose missing strips are remembered
-constexpr int kKvRawSlots = 3;    // ring of raw strips
-constexpr int kKvRawStrips = 4;   // strips of a slot
+constexpr int kKvChunkStrips = kKvChunk / kStripTokens;
+constexpr int kKvRawSlots = 3;  // chunks of raw strips
+constexpr int kKvBuffers = 4;   // chunks of K and of V in FP16
+constexpr int kKvMasks = 16;    // chunks whose missing strips are remembered
 
 template <int D>
 struct KvTilesCfg {
-  static constexpr int ATOMS = D / 64;                 // 64-element atoms of a row
-  static constexpr int ATOM = 128 * 128;               // 128 rows of 128 bytes
-  static constexpr int TILE = ATOMS * ATOM;            // Q, K or V of 128 rows, FP16
-  static constexpr int RAW = kKvRawStrips * strip_bytes(D);
-  // two tiles each of Q, K and V, the ring of raw strips
-  static constexpr int SMEM = 6 * TILE + kKvRawSlots * RAW + 1024;
-  // TMEM columns: S of both row tiles (128 each), O of both, then P of both (two
-  // FP16 a column) where there is room (D = 64); else P takes S's place
-  static constexpr bool P_APART = D == 64;
-  static constexpr int O_COL = 256;
-  static constexpr int P_COL = P_APART ? 256 + 2 * D : 0;
-  static constexpr int P_STEP = P_APART ? 64 : 128;
+  static constexpr int ATOMS = D / 64;  // 64-element atoms of a row
+  static constexpr int Q_ATOM = 128 * 128;
+  static constexpr int Q_TILE = ATOMS * Q_ATOM;  // 128 rows
+  static constexpr int KV_ATOM = kKvChunk * 128;
+  static constexpr int KV_TILE = ATOMS * KV_ATOM;  // 64 tokens of K or V
+  static constexpr int RAW = kKvChunkStrips * strip_bytes(D);
+  static constexpr int SMEM = 2 * Q_TILE + 2 * kKvBuffers * KV_TILE + kKvRawSlots * RAW + 1024;
+  static constexpr int O_COL = 256;  // TMEM columns: S (two buffers of 64) of both tiles, then O
   static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -142,13 +136,14 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t *sQ = smem;                // [2] tiles each
-  uint8_t *sK = sQ + 2 * C::TILE;
-  uint8_t *sV = sK + 2 * C::TILE;
-  uint8_t *sRaw = sV + 2 * C::TILE;  // [kKvRawSlots]
-  // [2]: by buffer (K, V) or by row tile (S, P, O)
-  __shared__ __align__(8) uint64_t raw_full[kKvRawSlots], raw_empty[kKvRawSlots], k_full[2],
-      k_empty[2], v_full[2], v_empty[2], s_full[2], s_read[2], p_full[2][2], pv_done[2], drain;
+  uint8_t *sQ = smem;                                // [2]
+  uint8_t *sK = sQ + 2 * C::Q_TILE;                  // [kKvBuffers]
+  uint8_t *sV = sK + kKvBuffers * C::KV_TILE;        // [kKvBuffers]
+  uint8_t *sRaw = sV + kKvBuffers * C::KV_TILE;      // [kKvRawSlots]
+  // S, P and the products with P: by row tile and buffer
+  __shared__ __align__(8) uint64_t raw_full[kKvRawSlots], raw_empty[kKvRawSlots],
+      k_full[kKvBuffers], k_empty[kKvBuffers], v_full[kKvBuffers], v_empty[kKvBuffers],
+      s_full[2][2], p_full[2][2], pv_done[2][2], drain[2];
   __shared__ uint32_t missing[kKvMasks];  // strips that the cache lacks, a bit each
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
@@ -161,18 +156,19 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
       mbar_init(&raw_full[s], 1);
       mbar_init(&raw_empty[s], 4);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kKvBuffers; ++s) {
       mbar_init(&k_full[s], 4);
       mbar_init(&k_empty[s], 1);
       mbar_init(&v_full[s], 4);
       mbar_init(&v_empty[s], 1);
-      mbar_init(&s_full[s], 1);
-      mbar_init(&s_read[s], 4);
-      mbar_init(&p_full[s][0], 4);
-      mbar_init(&p_full[s][1], 4);
-      mbar_init(&pv_done[s], 1);
     }
-    mbar_init(&drain, 1);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&s_full[s / 2][s % 2], 1);
+      mbar_init(&p_full[s / 2][s % 2], 4);
+      mbar_init(&pv_done[s / 2][s % 2], 1);
+    }
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     abort_word = 0;
     fence_mbar_init();
   }
@@ -228,7 +224,7 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
   const int row_tiles = rows > 128 ? 2 : 1;
   // tokens that some row of the block sees, and that all of them see
   const int most = kv_limit(req, (row0 + rows - 1) / a.group, a.causal);
-  const int tiles = (most + kKvTileTokens - 1) / kKvTileTokens;
+  const int chunks = (most + kKvChunk - 1) / kKvChunk;
 
   // A wait of the whole warp, and what follows when it runs out.
   auto wait = [&](uint64_t *bar, int n) {
@@ -240,29 +236,41 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
     return false;
   };
 
+  // The issuing threads' waits; and every MMA has retired before they go on.
+  auto wait1 = [&](uint64_t *bar, int n) -> bool {
+    if (mbar_wait_polled(bar, n & 1, abort_flag, timeout_ns)) {
+      tc_fence_after();
+      return true;
+    }
+    record_timeout(kSiteKvTiles);
+    *abort_flag = 1;
+    return false;
+  };
+  auto finish = [&](int which) {
+    umma_commit(&drain[which]);
+    int zero = 0;
+    if (!mbar_wait_bounded(&drain[which], 0, &zero, timeout_ns)) record_timeout(kSiteKvTiles);
+  };
+
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     const int32_t *table = a.table + static_cast<int64_t>(b) * a.width;
     const int strips = (most + kStripTokens - 1) / kStripTokens;
-    const int slots = (strips + kKvRawStrips - 1) / kKvRawStrips;
     auto page_of = [&](int strip) {
-      return lane < kKvRawStrips && strip < strips
+      return lane < kKvChunkStrips && strip < strips
                  ? table[(strip * kStripTokens) >> a.cache.page_shift]
                  : -1;
     };
     int page = page_of(lane);
     int i = 0;
-    for (; i < slots; ++i) {
+    for (; i < chunks; ++i) {
       const int slot = i % kKvRawSlots;
       if (!wait(&raw_empty[slot], i / kKvRawSlots + 1)) break;
-      const int strip = i * kKvRawStrips + lane;
+      const int strip = i * kKvChunkStrips + lane;
       const bool there = page >= 0 && page < a.cache.pages;
       const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there);
       if (lane == 0) {
-        // (the strips of the tile's second half are missing until told otherwise)
-        const uint32_t gone = ~mask & ((1u << kKvRawStrips) - 1);
-        uint32_t *word = &missing[i / 2 % kKvMasks];
-        *word = i & 1 ? (*word & 0x0Fu) | gone << kKvRawStrips : 0xF0u | gone;
+        missing[i % kKvMasks] = ~mask & ((1u << kKvChunkStrips) - 1);
         mbar_arrive_expect_tx(&raw_full[slot], __popc(mask) * strip_bytes(D));
       }
       __syncwarp();
@@ -274,99 +282,78 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
                      a.cache.data + at * strip_bytes(D), strip_bytes(D), &raw_full[slot],
                      l2_policy_evict_normal());
       }
-      page = page_of(strip + kKvRawStrips);
+      page = page_of(strip + kKvChunkStrips);
     }
-    if (i < slots) {  // copies in flight land before the block may end
+    if (i < chunks) {  // copies in flight land before the block may end
       int zero = 0;
       for (int k = max(i - kKvRawSlots, 0); k < i; ++k)
         mbar_wait_polled_warp(&raw_full[k % kKvRawSlots], k / kKvRawSlots & 1, &zero, timeout_ns);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issue
+    // ------------------------------------------------------------ scores
     asm volatile("bar.sync 1, 288;" ::: "memory");  // Q is there
-    if (lane == 0 && tiles > 0) {
-      constexpr uint32_t idesc_s = idesc_f16_f32(128, kKvTileTokens, false);
-      constexpr uint32_t idesc_o = idesc_f16_f32(128, D, true);
-      auto wait1 = [&](uint64_t *bar, int n) -> bool {
-        if (mbar_wait_polled(bar, n & 1, abort_flag, timeout_ns)) {
-          tc_fence_after();
-          return true;
-        }
-        record_timeout(kSiteKvTiles);
-        *abort_flag = 1;
-        return false;
-      };
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_f16_f32(128, kKvChunk, false);
       const uint32_t q_desc = desc_k_major(smem_u32(sQ)), k_desc = desc_k_major(smem_u32(sK));
-      const uint32_t v_desc = desc_mn_major(smem_u32(sV), C::ATOM);
-      // step n is row tile n % row_tiles at token tile n / row_tiles
-      const int steps = tiles * row_tiles;
-      auto scores = [&](int n) -> bool {  // S = Q_t K^T
-        const int t = n % row_tiles, j = n / row_tiles;
-        if (t == 0 && !wait1(&k_full[j & 1], j >> 1)) return false;
-        const uint32_t q = q_desc + t * (C::TILE >> 4), k = k_desc + (j & 1) * (C::TILE >> 4);
-        const uint32_t d = tmem + t * kKvTileTokens;
-        umma_f16_ss<false>(d, q, k, idesc_s);
-#pragma unroll
-        for (int x = 1; x < D / 16; ++x) {
-          const uint32_t at = (x / 4 * C::ATOM + x % 4 * 32) >> 4;
-          umma_f16_ss<true>(d, q + at, k + at, idesc_s);
-        }
-        umma_commit(&s_full[t]);
-        if (t == row_tiles - 1) umma_commit(&k_empty[j & 1]);
-        return true;
-      };
-      auto sums = [&](int n) -> bool {  // O_t += P_t V, P in two halves
-        const int t = n % row_tiles, j = n / row_tiles;
-        if (t == 0 && !wait1(&v_full[j & 1], j >> 1)) return false;
-        const uint32_t v = v_desc + (j & 1) * (C::TILE >> 4);
-        const uint32_t d = tmem + C::O_COL + t * D, p = tmem + C::P_COL + t * C::P_STEP;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!wait1(&p_full[t][h], j)) return false;
-#pragma unroll
-          for (int x = 0; x < kKvTileTokens / 32; ++x) {
-            const int k = h * (kKvTileTokens / 32) + x;
-            umma_f16_ts(d, p + k * 8, v + k * (2048 >> 4), idesc_o, k != 0 || j != 0);
-          }
-        }
-        umma_commit(&pv_done[t]);
-        if (t == row_tiles - 1) umma_commit(&v_empty[j & 1]);
-        return true;
-      };
       bool ok = true;
-      for (int n = 0; n < row_tiles && ok; ++n) ok = scores(n);
-      for (int n = 0; n < steps && ok; ++n) {
-        const int t = n % row_tiles, j = n / row_tiles;
-        const bool more = n + row_tiles < steps;
-        if constexpr (C::P_APART) {
-          // the next scores as soon as these are in registers
-          if (more) ok = wait1(&s_read[t], j) && scores(n + row_tiles);
-          if (ok) ok = sums(n);
-        } else {
-          ok = sums(n);
-          // P lies where the next scores go
-          if (ok && more) ok = wait1(&pv_done[t], j) && scores(n + row_tiles);
+      for (int i = 0; i < chunks && ok; ++i) {
+        const int buf = i % kKvBuffers;
+        ok = wait1(&k_full[buf], i / kKvBuffers);
+        for (int t = 0; t < row_tiles && ok; ++t) {  // S = Q_t K^T
+          // P of two chunks before lies there
+          if (i >= 2) ok = wait1(&pv_done[t][i & 1], (i - 2) >> 1);
+          if (!ok) break;
+          const uint32_t q = q_desc + t * (C::Q_TILE >> 4), k = k_desc + buf * (C::KV_TILE >> 4);
+          const uint32_t d = tmem + t * 128 + (i & 1) * 64;
+          umma_f16_ss<false>(d, q, k, idesc);
+#pragma unroll
+          for (int x = 1; x < D / 16; ++x)
+            umma_f16_ss<true>(d, q + ((x / 4 * C::Q_ATOM + x % 4 * 32) >> 4),
+                              k + ((x / 4 * C::KV_ATOM + x % 4 * 32) >> 4), idesc);
+          umma_commit(&s_full[t][i & 1]);
         }
+        if (ok) umma_commit(&k_empty[buf]);
       }
-      umma_commit(&drain);
-      int zero = 0;
-      if (!mbar_wait_bounded(&drain, 0, &zero, timeout_ns)) record_timeout(kSiteKvTiles);
+      finish(0);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ sums
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_f16_f32(128, D, true);
+      const uint32_t v_desc = desc_mn_major(smem_u32(sV), C::KV_ATOM);
+      bool ok = true;
+      for (int i = 0; i < chunks && ok; ++i) {
+        const int buf = i % kKvBuffers;
+        ok = wait1(&v_full[buf], i / kKvBuffers);
+        for (int t = 0; t < row_tiles && ok; ++t) {  // O_t += P_t V
+          ok = wait1(&p_full[t][i & 1], i >> 1);
+          if (!ok) break;
+          const uint32_t v = v_desc + buf * (C::KV_TILE >> 4);
+          const uint32_t d = tmem + C::O_COL + t * 128, p = tmem + t * 128 + (i & 1) * 64;
+#pragma unroll
+          for (int x = 0; x < kKvChunk / 16; ++x)
+            umma_f16_ts(d, p + x * 8, v + x * (2048 >> 4), idesc, x != 0 || i != 0);
+          umma_commit(&pv_done[t][i & 1]);
+        }
+        if (ok) umma_commit(&v_empty[buf]);
+      }
+      finish(1);
     }
     __syncwarp();
   } else if (warp >= 12) {
     // ------------------------------------------------------------ codes to FP16
     const int w = warp - 12;
     bool ok = true;
-    // this warp's strip of a slot: 16 tokens of K or V; row0 of the 128-token tile
-    auto convert = [&](const uint8_t *strip, uint8_t *tile, bool is_v, int row0, int tok0,
-                       bool gone) {
+    // this warp's strip of a chunk: 16 tokens of K or V
+    auto convert = [&](const uint8_t *strip, uint8_t *tile, bool is_v, int tok0, bool gone) {
       constexpr int LANES = D / 32;      // lanes of a row, 32 elements (16 bytes of codes) each
       constexpr int ROWS = 32 / LANES;   // rows of a round
       const int part = lane % LANES;
-#pragma unroll 1
+#pragma unroll
       for (int x = 0; x < kStripTokens / ROWS; ++x) {
         const int in = x * ROWS + lane / LANES;
-        const int row = row0 + in;
+        const int row = w * kStripTokens + in;
         const uint4 codes = *reinterpret_cast<const uint4 *>(strip + (is_v ? strip_v(D) : 0) +
                                                              in * (D / 2) + part * 16);
         uint32_t sc = *reinterpret_cast<const uint16_t *>(
@@ -389,7 +376,7 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
         // 16-byte units 4 (part % 2) + y of the row's 128 bytes in atom part / 2,
         // swizzled; the second atom's lanes go in another order, which keeps
         // the eight lanes of a store phase on eight different units
-        uint8_t *to = tile + part / 2 * C::ATOM + row * 128;
+        uint8_t *to = tile + part / 2 * C::KV_ATOM + row * 128;
         const int turn = part / 2 * 2;
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
@@ -400,38 +387,27 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
         }
       }
     };
-    const int slots = (most + kKvRawStrips * kStripTokens - 1) / (kKvRawStrips * kStripTokens);
-    for (int j = 0; j < tiles && ok; ++j) {
-      const int buf = j & 1, tok0 = j * kKvTileTokens;
-      uint8_t *k_tile = sK + buf * C::TILE, *v_tile = sV + buf * C::TILE;
-      // the products with the K and V two tiles before are done
-      ok = wait(&k_empty[buf], (j >> 1) + 1);
-      for (int h = 0; h < 2 && ok; ++h) {
-        const int i = 2 * j + h, slot = i % kKvRawSlots;
-        const int row0 = (h * kKvRawStrips + w) * kStripTokens;
-        const uint8_t *strip = sRaw + slot * C::RAW + w * strip_bytes(D);
-        bool gone = true;  // the last tile may lack its second slot
-        if (i < slots) {
-          ok = wait(&raw_full[slot], i / kKvRawSlots);
-          if (!ok) break;
-          gone = missing[j % kKvMasks] >> (h * kKvRawStrips + w) & 1u;
-          convert(strip, k_tile, false, row0, tok0, gone);
-        }
-        if (h == 1) {
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&k_full[buf]);
-        }
-        if (h == 0) ok = wait(&v_empty[buf], (j >> 1) + 1);
-        if (!ok) break;
-        convert(strip, v_tile, true, row0, tok0, gone);
-        if (h == 1) {
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&v_full[buf]);
-        }
-        __syncwarp();
-        if (i < slots && lane == 0) mbar_arrive(&raw_empty[slot]);
+    for (int i = 0; i < chunks && ok; ++i) {
+      const int slot = i % kKvRawSlots, buf = i % kKvBuffers, use = i / kKvBuffers;
+      const uint8_t *strip = sRaw + slot * C::RAW + w * strip_bytes(D);
+      ok = wait(&raw_full[slot], i / kKvRawSlots);
+      if (!ok) break;
+      const bool gone = missing[i % kKvMasks] >> w & 1u;
+      // the products with what the buffer held before are done
+      ok = wait(&k_empty[buf], use + 1);
+      if (!ok) break;
+      convert(strip, sK + buf * C::KV_TILE, false, i * kKvChunk, gone);
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_full[buf]);
+      ok = wait(&v_empty[buf], use + 1);
+      if (!ok) break;
+      convert(strip, sV + buf * C::KV_TILE, true, i * kKvChunk, gone);
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&v_full[buf]);
+        mbar_arrive(&raw_empty[slot]);
       }
     }
   } else if (warp >= 4) {
@@ -461,80 +437,65 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
       c = fmaxf(fabsf(factor) * __uint_as_float(static_cast<uint32_t>(127 + e) << 23), 0x1p-126f);
       const float down =
           copysignf(__uint_as_float(static_cast<uint32_t>(127 - e) << 23), factor);
-      uint8_t *to = sQ + tile * C::TILE + (quarter * 32 + lane) * 128;
+      uint8_t *to = sQ + tile * C::Q_TILE + (quarter * 32 + lane) * 128;
 #pragma unroll
       for (int x = 0; x < D / 8; ++x) {
         const uint4 h = make_uint4(pack_f16(bf16_lo(q[x].x) * down, bf16_hi(q[x].x) * down),
                                    pack_f16(bf16_lo(q[x].y) * down, bf16_hi(q[x].y) * down),
                                    pack_f16(bf16_lo(q[x].z) * down, bf16_hi(q[x].z) * down),
                                    pack_f16(bf16_lo(q[x].w) * down, bf16_hi(q[x].w) * down));
-        *reinterpret_cast<uint4 *>(to + x / 8 * C::ATOM + (((x % 8) ^ (lane & 7)) << 4)) = h;
+        *reinterpret_cast<uint4 *>(to + x / 8 * C::Q_ATOM + (((x % 8) ^ (lane & 7)) << 4)) = h;
       }
       fence_async_shared();
     }
     asm volatile("bar.sync 1, 288;" ::: "memory");  // with the MMA warp
     const bool used = tile < row_tiles;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t t_s = tmem + lanes + tile * kKvTileTokens;
-    const uint32_t t_p = tmem + lanes + C::P_COL + tile * C::P_STEP;
-    const uint32_t t_o = tmem + lanes + C::O_COL + tile * D;
+    const uint32_t t_o = tmem + lanes + C::O_COL + tile * 128;
     float neg_m = INFINITY, l = 0.0f;  // minus the maximum in log2 units, the sum
     bool ok = true;
-    for (int j = 0; used && j < tiles; ++j) {
-      ok = wait(&s_full[tile], j);
+    for (int i = 0; used && i < chunks; ++i) {
+      ok = wait(&s_full[tile][i & 1], i >> 1);
       if (!ok) break;
       tc_fence_after();
-      const int tok0 = j * kKvTileTokens;
-      const uint32_t gone = missing[j % kKvMasks];
-      const bool edge = __any_sync(0xFFFFFFFFu, tok0 + kKvTileTokens > lim) || gone != 0;
-      uint32_t s0[32], s1[32];  // scores of two 32-token chunks
-      // of an edge tile: a score that the row does not see is -inf
-      auto mask = [&](uint32_t (&s)[32], int tok, uint32_t gone) {
-        const int n0 = gone & 1u ? 0 : lim - tok, n1 = gone & 2u ? 0 : lim - tok;
+      const uint32_t t_s = tmem + lanes + tile * 128 + (i & 1) * 64;
+      uint32_t s0[32], s1[32];  // the scores of 32 tokens each
+      tmem_ld_32x32b_x32(t_s, s0);
+      tmem_ld_32x32b_x32(t_s + 32, s1);
+      const int tok0 = i * kKvChunk;
+      const uint32_t gone = missing[i % kKvMasks];
+      const bool edge = __any_sync(0xFFFFFFFFu, tok0 + kKvChunk > lim) || gone != 0;
+      tmem_ld_wait();
+      if (edge) {  // a score that the row does not see is -inf
+        auto mask = [&](uint32_t (&s)[32], int tok, uint32_t gone) {
+          const int n0 = gone & 1u ? 0 : lim - tok, n1 = gone & 2u ? 0 : lim - tok;
 #pragma unroll
-        for (int x = 0; x < 32; ++x)
-          if (x >= (x < kStripTokens ? n0 : n1)) s[x] = 0xFF800000u;
-      };
-      auto largest = [&](const uint32_t (&s)[32], float top) {
-        float other = top;
-#pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          top = fmaxf(top, __uint_as_float(s[x]));
-          other = fmaxf(other, __uint_as_float(s[x + 1]));
-        }
-        return fmaxf(top, other);
-      };
-      auto load = [&](int h) {  // the scores of 64 tokens
-        tmem_ld_32x32b_x32(t_s + h * 64, s0);
-        tmem_ld_32x32b_x32(t_s + h * 64 + 32, s1);
-        tmem_ld_wait();
-        if (edge) {
-          mask(s0, tok0 + h * 64, gone >> (4 * h));
-          mask(s1, tok0 + h * 64 + 32, gone >> (4 * h + 2));
-        }
-      };
-      float top = -INFINITY;
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        load(h);
-        top = largest(s1, largest(s0, top));
+          for (int x = 0; x < 32; ++x)
+            if (x >= (x < kStripTokens ? n0 : n1)) s[x] = 0xFF800000u;
+        };
+        mask(s0, tok0, gone);
+        mask(s1, tok0 + 32, gone >> 2);
       }
+      float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int x = 0; x < 32; x += 2) {
+        tops[0] = fmaxf(tops[0], __uint_as_float(s0[x]));
+        tops[1] = fmaxf(tops[1], __uint_as_float(s0[x + 1]));
+        tops[2] = fmaxf(tops[2], __uint_as_float(s1[x]));
+        tops[3] = fmaxf(tops[3], __uint_as_float(s1[x + 1]));
+      }
+      const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
       const float now = top == -INFINITY ? -INFINITY : top * c;
-      // P's columns, where they are not S's, and O's, where they are to be scaled,
-      // are in use until the last products are done
-      const bool move = __any_sync(0xFFFFFFFFu, now + neg_m > kKvSlack);
-      if (j > 0 && (move || C::P_APART)) {
-        ok = wait(&pv_done[tile], j - 1);
-        if (!ok) break;
-        tc_fence_after();
-      }
-      if (move) {
-        // move the maxima (at first from -inf)
+      if (__any_sync(0xFFFFFFFFu, now + neg_m > kKvSlack)) {
+        // move the maxima (at first from -inf); O must not be in use
         const float next = fmaxf(-neg_m, now);
         const float by = next == -INFINITY ? 1.0f : ex2_approx(-neg_m - next);
         neg_m = next == -INFINITY ? INFINITY : -next;
         l *= by;
-        if (j > 0) {
+        if (i > 0) {
+          ok = wait(&pv_done[tile][(i - 1) & 1], (i - 1) >> 1);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll 1
           for (int col = 0; col < D; col += 16) {
             uint32_t o[16];
@@ -549,7 +510,7 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
       // a row that has seen nothing yet has no maximum: any, for weights of 0
       const float shift = neg_m == INFINITY ? 0.0f : neg_m;
       float sums[2] = {0.0f, 0.0f};
-      // weights of a chunk, rounded to FP16 (2^-11 of each) for the second product
+      // weights, rounded to FP16 (2^-11 of each) for the second product
       auto weigh = [&](const uint32_t (&s)[32], uint32_t col) {
         uint32_t p[16];
 #pragma unroll
@@ -562,25 +523,16 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
         }
         tmem_st_32x32b_x16(col, p);
       };
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        load(h);
-        if (C::P_APART && h == 1) {  // the columns may take the next scores
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_read[tile]);
-        }
-        weigh(s0, t_p + h * 32);
-        weigh(s1, t_p + h * 32 + 16);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[tile][h]);  // 64 tokens' weights are there
-      }
+      weigh(s0, t_s);
+      weigh(s1, t_s + 16);
       l += sums[0] + sums[1];
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[tile][i & 1]);
     }
-    if (used && ok && tiles > 0) {
-      ok = wait(&pv_done[tile], tiles - 1);
+    if (used && ok && chunks > 0) {
+      ok = wait(&pv_done[tile][(chunks - 1) & 1], (chunks - 1) >> 1);
       tc_fence_after();
     }
     if (used && ok) {
@@ -589,7 +541,7 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
 #pragma unroll 1
       for (int col = 0; col < D; col += 32) {
         uint32_t o[32];
-        if (tiles > 0) {
+        if (chunks > 0) {
           tmem_ld_32x32b_x32(t_o + col, o);
           tmem_ld_wait();
         }
@@ -598,7 +550,7 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
           float v[8];
 #pragma unroll
           for (int y = 0; y < 8; ++y)
-            v[y] = tiles > 0 && l != 0.0f ? __uint_as_float(o[x + y]) * by : 0.0f;
+            v[y] = chunks > 0 && l != 0.0f ? __uint_as_float(o[x + y]) * by : 0.0f;
           if (!live) continue;
           if (a.s_out) {
             *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + at * D + col + x) =
