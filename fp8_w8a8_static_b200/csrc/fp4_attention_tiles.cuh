@@ -75,26 +75,45 @@ __device__ __forceinline__ uint32_t desc_mn_major(uint32_t saddr, uint32_t block
   return saddr >> 4 | block >> 4 << 16;
 }
 
+// Executed by the whole warp, issued by the lane with leader != 0: the operands
+// stay warp-uniform.
 template <bool ACC>
-__device__ __forceinline__ void umma_f16_ss(uint32_t tmem_d, uint32_t a_low, uint32_t b_low,
-                                            uint32_t idesc) {
+__device__ __forceinline__ void umma_f16_ss(uint32_t leader, uint32_t tmem_d, uint32_t a_low,
+                                            uint32_t b_low, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t"
       "mov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
-      "setp.ne.b32 p, %5, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(a_low), "r"(b_low), "r"(idesc), "n"(kDescHigh), "n"(ACC ? 1 : 0));
+      "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(a_low), "r"(b_low), "r"(idesc), "n"(kDescHigh), "n"(ACC ? 1 : 0), "r"(leader));
 }
 
 // A from TMEM: lane = row, a column holds two neighbouring elements.
-__device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_low,
-                                            uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void umma_f16_ts(uint32_t leader, uint32_t tmem_d, uint32_t tmem_a,
+                                            uint32_t b_low, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\t"
       "mov.b64 b, {%2, %4};\n\t"
-      "setp.ne.b32 p, %5, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "r"(b_low), "r"(idesc), "n"(kDescHigh), "r"(accumulate));
+      "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "r"(b_low), "r"(idesc), "n"(kDescHigh), "r"(accumulate), "r"(leader));
+}
+
+__device__ __forceinline__ void umma_commit_by(uint32_t leader, uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar)),
+      "r"(leader)
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e;
 }
 
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -236,20 +255,17 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
     return false;
   };
 
-  // The issuing threads' waits; and every MMA has retired before they go on.
-  auto wait1 = [&](uint64_t *bar, int n) -> bool {
-    if (mbar_wait_polled(bar, n & 1, abort_flag, timeout_ns)) {
-      tc_fence_after();
-      return true;
-    }
-    record_timeout(kSiteKvTiles);
-    *abort_flag = 1;
-    return false;
+  // The issuing warps' waits; and every MMA has retired before they go on.
+  auto wait_mma = [&](uint64_t *bar, int n) {
+    const bool ok = wait(bar, n);
+    tc_fence_after();
+    return ok;
   };
-  auto finish = [&](int which) {
-    umma_commit(&drain[which]);
+  auto finish = [&](uint32_t leader, int which) {
+    umma_commit_by(leader, &drain[which]);
     int zero = 0;
-    if (!mbar_wait_bounded(&drain[which], 0, &zero, timeout_ns)) record_timeout(kSiteKvTiles);
+    if (!mbar_wait_polled_warp(&drain[which], 0, &zero, timeout_ns) && lane == 0)
+      record_timeout(kSiteKvTiles);
   };
 
   if (warp == 0) {
@@ -292,55 +308,58 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ scores
     asm volatile("bar.sync 1, 288;" ::: "memory");  // Q is there
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_f16_f32(128, kKvChunk, false);
-      const uint32_t q_desc = desc_k_major(smem_u32(sQ)), k_desc = desc_k_major(smem_u32(sK));
-      bool ok = true;
-      for (int i = 0; i < chunks && ok; ++i) {
-        const int buf = i % kKvBuffers;
-        ok = wait1(&k_full[buf], i / kKvBuffers);
-        for (int t = 0; t < row_tiles && ok; ++t) {  // S = Q_t K^T
-          // P of two chunks before lies there
-          if (i >= 2) ok = wait1(&pv_done[t][i & 1], (i - 2) >> 1);
-          if (!ok) break;
-          const uint32_t q = q_desc + t * (C::Q_TILE >> 4), k = k_desc + buf * (C::KV_TILE >> 4);
-          const uint32_t d = tmem + t * 128 + (i & 1) * 64;
-          umma_f16_ss<false>(d, q, k, idesc);
+    // (a broadcast value is known to be the same for the whole warp)
+    const int n = __shfl_sync(0xFFFFFFFFu, chunks, 0);
+    const int n_t = __shfl_sync(0xFFFFFFFFu, row_tiles, 0);
+    const uint32_t base = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    const uint32_t leader = elect_one();
+    constexpr uint32_t idesc = idesc_f16_f32(128, kKvChunk, false);
+    const uint32_t q_desc = desc_k_major(smem_u32(sQ)), k_desc = desc_k_major(smem_u32(sK));
+    bool ok = true;
+    for (int i = 0; i < n && ok; ++i) {
+      const int buf = i % kKvBuffers;
+      ok = wait_mma(&k_full[buf], i / kKvBuffers);
+      for (int t = 0; t < n_t && ok; ++t) {  // S = Q_t K^T
+        // P of two chunks before lies there
+        if (i >= 2) ok = wait_mma(&pv_done[t][i & 1], (i - 2) >> 1);
+        if (!ok) break;
+        const uint32_t q = q_desc + t * (C::Q_TILE >> 4), k = k_desc + buf * (C::KV_TILE >> 4);
+        const uint32_t d = base + t * 128 + (i & 1) * 64;
+        umma_f16_ss<false>(leader, d, q, k, idesc);
 #pragma unroll
-          for (int x = 1; x < D / 16; ++x)
-            umma_f16_ss<true>(d, q + ((x / 4 * C::Q_ATOM + x % 4 * 32) >> 4),
-                              k + ((x / 4 * C::KV_ATOM + x % 4 * 32) >> 4), idesc);
-          umma_commit(&s_full[t][i & 1]);
-        }
-        if (ok) umma_commit(&k_empty[buf]);
+        for (int x = 1; x < D / 16; ++x)
+          umma_f16_ss<true>(leader, d, q + ((x / 4 * C::Q_ATOM + x % 4 * 32) >> 4),
+                            k + ((x / 4 * C::KV_ATOM + x % 4 * 32) >> 4), idesc);
+        umma_commit_by(leader, &s_full[t][i & 1]);
       }
-      finish(0);
+      if (ok) umma_commit_by(leader, &k_empty[buf]);
     }
-    __syncwarp();
+    finish(leader, 0);
   } else if (warp == 2) {
     // ------------------------------------------------------------ sums
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_f16_f32(128, D, true);
-      const uint32_t v_desc = desc_mn_major(smem_u32(sV), C::KV_ATOM);
-      bool ok = true;
-      for (int i = 0; i < chunks && ok; ++i) {
-        const int buf = i % kKvBuffers;
-        ok = wait1(&v_full[buf], i / kKvBuffers);
-        for (int t = 0; t < row_tiles && ok; ++t) {  // O_t += P_t V
-          ok = wait1(&p_full[t][i & 1], i >> 1);
-          if (!ok) break;
-          const uint32_t v = v_desc + buf * (C::KV_TILE >> 4);
-          const uint32_t d = tmem + C::O_COL + t * 128, p = tmem + t * 128 + (i & 1) * 64;
+    const int n = __shfl_sync(0xFFFFFFFFu, chunks, 0);
+    const int n_t = __shfl_sync(0xFFFFFFFFu, row_tiles, 0);
+    const uint32_t base = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+    const uint32_t leader = elect_one();
+    constexpr uint32_t idesc = idesc_f16_f32(128, D, true);
+    const uint32_t v_desc = desc_mn_major(smem_u32(sV), C::KV_ATOM);
+    bool ok = true;
+    for (int i = 0; i < n && ok; ++i) {
+      const int buf = i % kKvBuffers;
+      ok = wait_mma(&v_full[buf], i / kKvBuffers);
+      for (int t = 0; t < n_t && ok; ++t) {  // O_t += P_t V
+        ok = wait_mma(&p_full[t][i & 1], i >> 1);
+        if (!ok) break;
+        const uint32_t v = v_desc + buf * (C::KV_TILE >> 4);
+        const uint32_t d = base + C::O_COL + t * 128, p = base + t * 128 + (i & 1) * 64;
 #pragma unroll
-          for (int x = 0; x < kKvChunk / 16; ++x)
-            umma_f16_ts(d, p + x * 8, v + x * (2048 >> 4), idesc, x != 0 || i != 0);
-          umma_commit(&pv_done[t][i & 1]);
-        }
-        if (ok) umma_commit(&v_empty[buf]);
+        for (int x = 0; x < kKvChunk / 16; ++x)
+          umma_f16_ts(leader, d, p + x * 8, v + x * (2048 >> 4), idesc, x != 0 || i != 0);
+        umma_commit_by(leader, &pv_done[t][i & 1]);
       }
-      finish(1);
+      if (ok) umma_commit_by(leader, &v_empty[buf]);
     }
-    __syncwarp();
+    finish(leader, 1);
   } else if (warp >= 12) {
     // ------------------------------------------------------------ codes to FP16
     const int w = warp - 12;
