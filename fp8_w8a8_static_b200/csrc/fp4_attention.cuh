@@ -34,10 +34,10 @@
 
 namespace fp8ws {
 
-constexpr int kKvRowWarps = 4;                             // consumers
-constexpr int kKvRowThreads = (kKvRowWarps + 1) * 32;      // and one producer warp
+constexpr int kKvRowWarps = 4;
+constexpr int kKvRowThreads = kKvRowWarps * 32;
 constexpr int kKvChunk = 64;     // tokens of a unit
-constexpr int kKvSlots = 12;     // ring slots of a block, up to 2 strips each
+constexpr int kKvSlots = 3;      // ring slots of a warp, up to 2 strips each
 constexpr int kKvMaxBlocks = 444;  // ranges at most: 148 SMs x 3 blocks
 // Blocks of an SM: 16 query rows take the registers of two (168 spill).
 __host__ __device__ constexpr int kv_blocks_per_sm(int NT) { return NT == 1 ? 3 : 2; }
@@ -150,15 +150,10 @@ template <int D, int NT>
 struct KvRowsCfg {
   static constexpr int ROWS = 8 * NT;
   static constexpr int SLOT = 2 * strip_bytes(D);
-  static constexpr int RING = kKvSlots * SLOT;
+  static constexpr int RING = kKvRowWarps * kKvSlots * SLOT;
   static constexpr int MERGE = kKvRowWarps * ROWS * (D + 2) * 4;
   static constexpr int SMEM = RING + MERGE;
 };
-
-// Barrier of the consumer warps alone.
-__device__ __forceinline__ void consumers_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(kKvRowWarps * 32) : "memory");
-}
 
 // One part of a block's range: units [k0, k1) of a (request, head, row tile).
 struct KvSegment {
@@ -170,8 +165,7 @@ struct KvSegment {
   int per_slot;        // strips of a ring slot: few of them are spread over the warps
 };
 
-// Walks a block's range segment by segment; the producer and the consumers
-// walk it alike.
+// Walks a block's range segment by segment; its warps walk it alike.
 template <int ROWS>
 struct KvWalk {
   const KvAttnArgs &a;
@@ -223,20 +217,17 @@ __global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
   constexpr int KB = D / 8;    // code bytes of a row that a thread holds (K), D/8 elements of V
   constexpr int TILES = D / 16;  // K steps of the first product, 16-row tiles of the second
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t full[kKvSlots], empty[kKvSlots];
-  __shared__ uint32_t present[kKvSlots];  // which strips of a slot exist
+  __shared__ __align__(8) uint64_t full[kKvRowWarps][kKvSlots];
   __shared__ int abort_flag;
   __shared__ int64_t s_first[3];  // units before request b0; in all; b0
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int g = lane / 4, t = lane % 4;  // fragment coordinates
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kKvSlots; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
-    abort_flag = 0;
+  if (lane == 0) {
+    for (int s = 0; s < kKvSlots; ++s) mbar_init(&full[warp][s], 1);
     fence_mbar_init();
   }
+  if (threadIdx.x == 0) abort_flag = 0;
   pdl_launch_dependents();
   pdl_wait();
 
@@ -282,74 +273,63 @@ __global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
   const int64_t per = (all + gridDim.x - 1) / gridDim.x;
   const int64_t begin = per * blockIdx.x;
   KvWalk<ROWS> walk{a, begin, min(begin + per, all), s_first[0], static_cast<int>(s_first[2])};
-  KvSegment seg;
-  uint32_t seq0 = 0;  // ring slots used by the segments before
+  if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
 
-  if (warp == kKvRowWarps) {
-    // ------------------------------------------------------------ producer
-    const uint64_t policy = l2_policy_evict_first();
-    bool ok = true;
-    while (ok && walk.next(seg)) {
-      const int32_t *table = a.table + static_cast<int64_t>(seg.b) * a.width;
-      auto page_of = [&](int strip) {
-        return strip < seg.strip1 ? table[(strip * kStripTokens) >> a.cache.page_shift] : -1;
-      };
-      const int S = seg.per_slot;
-      int page = page_of(seg.strip0 + lane);
-      for (int base = seg.strip0; base < seg.strip1 && ok; base += 32) {
-        const int strip = base + lane;  // each lane has one of 32 strips
-        const bool there = page >= 0 && page < a.cache.pages;
-        const uint8_t *src =
-            a.cache.data +
-            (((static_cast<int64_t>(there ? page : 0) * a.cache.heads + seg.head)
-              << (a.cache.page_shift - 4)) +
-             (strip & ((1 << (a.cache.page_shift - 4)) - 1))) *
-                strip_bytes(D);
-        const uint32_t exist = __ballot_sync(0xFFFFFFFFu, there);
-        page = page_of(strip + 32);
-        const int slots = (min(32, seg.strip1 - base) + S - 1) / S;
-        for (int i = 0; i < slots; ++i) {
-          const uint32_t seq = seq0++;
-          const uint32_t slot = seq % kKvSlots;
-          if (!mbar_wait_polled_warp(&empty[slot], (seq / kKvSlots & 1u) ^ 1u, &abort_flag,
-                                      timeout_ns)) {
-            if (lane == 0) {
-              record_timeout(kSiteKvRows);
-              *const_cast<volatile int *>(&abort_flag) = 1;
-            }
-            ok = false;
-            --seq0;
-            break;
-          }
-          const uint32_t mask = exist >> (i * S) & (S == 2 ? 3u : 1u);
-          if (lane == 0) {
-            present[slot] = mask;
-            mbar_arrive_expect_tx(&full[slot], __popc(mask) * strip_bytes(D));
-          }
-          __syncwarp();
-          if (lane / S == i && there)
-            bulk_load_1d(smem + slot * C::SLOT + (lane % S) * strip_bytes(D), src, strip_bytes(D),
-                         &full[slot], policy);
-        }
-      }
+  // The warp's ring.  Step n of a part is its strips strip0 + (n x 4 + warp) x S,
+  // S = per_slot; lanes 2k and 2k + 1 look up, for 16 steps at a time, the pages
+  // of step k's strips and start their copies.
+  uint8_t *ring = smem + warp * kKvSlots * C::SLOT;
+  const uint64_t policy = l2_policy_evict_first();
+  const uint8_t *src = nullptr;  // this lane's strip
+  bool there = false;
+  uint32_t exist = 0;     // lanes whose strip is there
+  uint32_t present = 0;   // two bits a slot: the strips that were copied
+  int put = 0, take = 0;  // next slot to fill and to read
+  uint32_t phase = 0;     // of the slots to be read, a bit each
+  int in_flight = 0;
+  auto fetch = [&](const KvSegment &s, int step) {
+    const int k = step % 16;
+    if (k == 0) {
+      const int strip = s.strip0 + ((step + lane / 2) * kKvRowWarps + warp) * s.per_slot + (lane & 1);
+      int page = -1;
+      if ((lane & 1) < s.per_slot && strip < s.strip1)
+        page = a.table[static_cast<int64_t>(s.b) * a.width +
+                       ((strip * kStripTokens) >> a.cache.page_shift)];
+      there = page >= 0 && page < a.cache.pages;
+      exist = __ballot_sync(0xFFFFFFFFu, there);
+      src = a.cache.data + (((static_cast<int64_t>(there ? page : 0) * a.cache.heads + s.head)
+                             << (a.cache.page_shift - 4)) +
+                            (strip & ((1 << (a.cache.page_shift - 4)) - 1))) *
+                               strip_bytes(D);
     }
-    if (!ok) {  // copies in flight land before the block may end
-      int zero = 0;
-      for (uint32_t k = seq0 > kKvSlots ? seq0 - kKvSlots : 0; k < seq0; ++k)
-        mbar_wait_polled_warp(&full[k % kKvSlots], k / kKvSlots & 1u, &zero, timeout_ns);
-    }
-    return;
-  }
+    const uint32_t mask = exist >> (2 * k) & 3u;
+    if (lane == 0) mbar_arrive_expect_tx(&full[warp][put], __popc(mask) * strip_bytes(D));
+    __syncwarp();
+    if (lane / 2 == k && there)
+      bulk_load_1d(ring + put * C::SLOT + (lane & 1) * strip_bytes(D), src, strip_bytes(D),
+                   &full[warp][put], policy);
+    present = (present & ~(3u << (2 * put))) | mask << (2 * put);
+    put = put == kKvSlots - 1 ? 0 : put + 1;
+    ++in_flight;
+  };
+  auto steps_of = [&](const KvSegment &s) {
+    const int mine = s.strip1 - s.strip0 - warp * s.per_slot;  // strips from the first one on
+    return mine <= 0 ? 0 : (mine - 1) / (kKvRowWarps * s.per_slot) + 1;
+  };
+  auto prime = [&](const KvSegment &s) {
+    const int steps = steps_of(s);
+    for (int n = 0; n < kKvSlots && n < steps; ++n) fetch(s, n);
+  };
 
-  // -------------------------------------------------------------- consumers
-  const int g = lane / 4, t = lane % 4;  // fragment coordinates
   float *mo = reinterpret_cast<float *>(smem + C::RING);  // [warp][row][D]
   float *ml = mo + kKvRowWarps * ROWS * D;                // [warp][row][2]
   const float c2 = a.scale * 1.4426950408889634f * __ldg(a.s_k);
   const float out_by = a.s_out ? __ldg(a.s_v) / __ldg(a.s_out) : __ldg(a.s_v);
   bool ok = true;
-  if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  while (walk.next(seg)) {
+  KvSegment seg, after;
+  bool more = walk.next(seg);
+  if (more) prime(seg);
+  for (; more; seg = after) {
     const KvRequest req = seg.req;
     const int head = seg.head;
     const int row0 = seg.tile * ROWS;
@@ -589,12 +569,9 @@ __global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
       }
     };
 
-    const int S = seg.per_slot;
-    const int slots = (seg.strip1 - seg.strip0 + S - 1) / S;
-    for (int i = warp; i < slots && ok; i += kKvRowWarps) {
-      const uint32_t seq = seq0 + i;
-      const uint32_t slot = seq % kKvSlots;
-      if (!mbar_wait_polled_warp(&full[slot], seq / kKvSlots & 1u, &abort_flag, timeout_ns)) {
+    const int S = seg.per_slot, steps = steps_of(seg);
+    for (int step = 0; step < steps && ok; ++step) {
+      if (!mbar_wait_polled_warp(&full[warp][take], phase >> take & 1u, &abort_flag, timeout_ns)) {
         if (lane == 0) {
           record_timeout(kSiteKvRows);
           *const_cast<volatile int *>(&abort_flag) = 1;
@@ -602,9 +579,9 @@ __global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
         ok = false;
         break;
       }
-      const uint32_t mask = present[slot];
-      const uint8_t *at = smem + slot * C::SLOT;
-      const int tok0 = (seg.strip0 + i * S) * kStripTokens;
+      const uint32_t mask = present >> (2 * take) & 3u;
+      const uint8_t *at = ring + take * C::SLOT;
+      const int tok0 = (seg.strip0 + (step * kKvRowWarps + warp) * S) * kStripTokens;
       // two strips at once, but for 16 rows of 128, whose sums take the registers
       if (NT * D <= 128 && mask == 3u) {
         multiply(std::integral_constant<int, 2>{}, at, tok0);
@@ -615,10 +592,12 @@ __global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
             multiply(std::integral_constant<int, 1>{}, at + x * strip_bytes(D),
                      tok0 + x * kStripTokens);
       }
+      phase ^= 1u << take;
+      take = take == kKvSlots - 1 ? 0 : take + 1;
+      --in_flight;
       __syncwarp();  // the slot is read: it may be filled again
-      if (lane == 0) mbar_arrive(&empty[slot]);
+      if (step + kKvSlots < steps) fetch(seg, step + kKvSlots);
     }
-    seq0 += slots;
 
     // ---------------------------------------------- the four warps' sums
 #pragma unroll
@@ -638,13 +617,16 @@ __global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
               make_float2(o[n][x][y], o[n][x][y + 2]);
       }
     }
-    consumers_sync();
+    // the next part's first copies run during the rest of this one
+    more = walk.next(after);
+    if (more && ok) prime(after);
+    __syncthreads();
     const bool whole = seg.k0 == 0 && seg.k1 == seg.chunks;
     // partial sums: slot 2c for the segment that block c's range starts in,
     // 2c + 1 for one that starts inside the range
     const int64_t piece = 2 * static_cast<int64_t>(blockIdx.x) + (seg.first == begin ? 0 : 1);
     float *pml = a.part + 2 * static_cast<int64_t>(gridDim.x) * ROWS * D;
-    for (int x = threadIdx.x; x < rows * (D / 4); x += kKvRowWarps * 32) {
+    for (int x = threadIdx.x; x < rows * (D / 4); x += kKvRowThreads) {
       const int row = x / (D / 4), d = 4 * (x % (D / 4));
       float top = -INFINITY;
 #pragma unroll
@@ -677,7 +659,7 @@ __global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
         }
       }
     }
-    consumers_sync();  // the sums are read: they may be overwritten
+    __syncthreads();  // the sums are read: they may be overwritten
     // The first boundary inside a segment is where it is merged: block c,
     // whose range starts inside the segment, if block c - 1's did not.
     if (!whole && seg.first == begin && seg.k0 > 0 && threadIdx.x == 0) {
@@ -689,6 +671,12 @@ __global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
             make_int4(seg.b, head, seg.tile * 2 + head_piece, static_cast<int>(last_block));
       }
     }
+  }
+  // after a wait that ran out: copies in flight land before the block ends
+  for (int zero = 0; in_flight > 0; --in_flight) {
+    mbar_wait_polled_warp(&full[warp][take], phase >> take & 1u, &zero, timeout_ns);
+    phase ^= 1u << take;
+    take = take == kKvSlots - 1 ? 0 : take + 1;
   }
 }
 
