@@ -92,8 +92,16 @@ __device__ __forceinline__ int kv_limit(const KvRequest &r, int i, int causal) {
 
 // What a segment costs beside its chunks (its queries' loads, the warps' sums),
 // in chunks: with ranges cut by chunks alone, the blocks that got many short
-// requests ended last (attend 48 requests of 17 to 6000 tokens: 67 us).
-constexpr int kKvSegmentCost = 2;
+// requests ended last (48 requests of 17 to 6000 tokens: 57 us with 2, 45 with 6,
+// 48 with 12).
+constexpr int kKvSegmentCost = 6;
+
+// Units of a block at least: a range costs its piece in the merge, too (one
+// request of 8000 tokens, 4 heads: 19.6 us with 1, 16.0 with 4).
+constexpr int kKvLeastUnits = 4;
+__device__ __forceinline__ int64_t kv_range(int64_t all) {
+  return max((all + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(kKvLeastUnits));
+}
 
 // Units of a request's row tiles over all heads: 64-token chunks (one at
 // least, so that rows without tokens are written too) and the fixed cost,
@@ -238,7 +246,7 @@ __global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
     for (int b = lane; b < a.batch; b += 32) all += kv_units<ROWS>(a, b, tiles, chunks);
 #pragma unroll
     for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
-    const int64_t per = (all + gridDim.x - 1) / gridDim.x;
+    const int64_t per = kv_range(all);
     const int64_t begin = per * blockIdx.x;
     int64_t before = 0;
     int b0 = 0;
@@ -270,7 +278,7 @@ __global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
   }
   __syncthreads();
   const int64_t all = s_first[1];
-  const int64_t per = (all + gridDim.x - 1) / gridDim.x;
+  const int64_t per = kv_range(all);
   const int64_t begin = per * blockIdx.x;
   KvWalk<ROWS> walk{a, begin, min(begin + per, all), s_first[0], static_cast<int>(s_first[2])};
   if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -404,8 +412,10 @@ __global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
 
     // NS neighbouring strips of shared memory at once (the second one's
     // arithmetic fills the first one's waits)
-    auto multiply = [&](auto ns, const uint8_t *strips, int tok0) {
+    // EDGE: some row does not see all of the tokens.
+    auto multiply = [&](auto ns, auto at_edge, const uint8_t *strips, int tok0) {
       constexpr int NS = decltype(ns)::value;
+      constexpr bool EDGE = decltype(at_edge)::value;
       // ---------------------------------------------- S^T = K Q^T
       float s[NS][NT][4];
 #pragma unroll
@@ -457,7 +467,6 @@ __global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
         }
       }
       // ---------------------------------------------- softmax
-      const bool edge = tok0 + NS * kStripTokens > all_see;
       uint32_t p[NS][NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -468,7 +477,7 @@ __global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               e[z][y] = fmaf(s[z][n][y], cq[n][y & 1], neg_m[n][y & 1]);
-              if (edge && tok0 + z * kStripTokens + g + 8 * (y >> 1) >= lim[n][y & 1])
+              if (EDGE && tok0 + z * kStripTokens + g + 8 * (y >> 1) >= lim[n][y & 1])
                 e[z][y] = -INFINITY;
             }
         };
@@ -541,7 +550,7 @@ __global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
             sc[h] = vs[row * 4 + g / 2];
           }
         }
-        if (tok0 + (z + 1) * kStripTokens > req.kv) {
+        if (EDGE) {
           // places past the last token hold anything, a NaN scale too
 #pragma unroll
           for (int h = 0; h < 4; ++h)
@@ -583,13 +592,18 @@ __global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
       const uint8_t *at = ring + take * C::SLOT;
       const int tok0 = (seg.strip0 + (step * kKvRowWarps + warp) * S) * kStripTokens;
       // two strips at once, but for 16 rows of 128, whose sums take the registers
-      if (NT * D <= 128 && mask == 3u) {
-        multiply(std::integral_constant<int, 2>{}, at, tok0);
+      constexpr int NS = NT * D <= 128 ? 2 : 1;
+      if (mask == (NS == 2 ? 3u : mask) && tok0 + 2 * kStripTokens <= all_see) {
+#pragma unroll 1
+        for (int x = 0; x < 2; x += NS)
+          if (mask >> x & 1u)
+            multiply(std::integral_constant<int, NS>{}, std::false_type{},
+                     at + x * strip_bytes(D), tok0 + x * kStripTokens);
       } else {
 #pragma unroll 1
         for (int x = 0; x < 2; ++x)
           if (mask >> x & 1u)
-            multiply(std::integral_constant<int, 1>{}, at + x * strip_bytes(D),
+            multiply(std::integral_constant<int, 1>{}, std::true_type{}, at + x * strip_bytes(D),
                      tok0 + x * kStripTokens);
       }
       phase ^= 1u << take;
@@ -682,8 +696,8 @@ __global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
 
 // Adds the partial sums of a segment that several blocks worked on, in block
 // order.  Block c merges the segment whose first block is c - 1.  All latency:
-// a thread owns 4 of a row's D values and every SPLIT-th piece, whose
-// loads do not depend on one another, and the shares meet in shared memory.
+// a thread owns 4 of a row's D values and every SPLIT-th piece, whose loads do
+// not depend on one another, and the shares meet in shared memory.
 constexpr int kKvMergeThreads = 512;
 
 template <int D, int NT>
@@ -692,8 +706,9 @@ __global__ void __launch_bounds__(kKvMergeThreads)
   constexpr int ROWS = 8 * NT;
   constexpr int LANES = D / 4;
   constexpr int SPLIT = kKvMergeThreads / (ROWS * LANES);
+  constexpr int RUN = 2;  // pieces of a thread in flight (more cost blocks an SM)
   __shared__ float4 s_val[SPLIT][ROWS][LANES];
-  __shared__ float s_sum[SPLIT][ROWS];
+  __shared__ float2 s_sum[SPLIT][ROWS];  // maximum, sum
   pdl_launch_dependents();
   pdl_wait();
   const int4 w = a.meta[blockIdx.x + 1];
@@ -704,41 +719,44 @@ __global__ void __launch_bounds__(kKvMergeThreads)
   const int rows = min(ROWS, req.q_len * a.group - row0);
   const int lane = threadIdx.x % LANES, row = threadIdx.x / LANES % ROWS;
   const int share = threadIdx.x / (LANES * ROWS);
-  const float *pml = a.part + 2 * static_cast<int64_t>(blocks) * ROWS * D;
-  // piece of block c: the first block's may be its second one
-  auto piece = [&](int c) {
-    return (2 * static_cast<int64_t>(c) + (c == first ? (w.z & 1) : 0)) * ROWS + row;
-  };
-  float top = -INFINITY;
-#pragma unroll 8
-  for (int c = first; c <= last; ++c) top = fmaxf(top, pml[2 * piece(c)]);
-  const float base = top == -INFINITY ? 0.0f : top;
-  float sum = 0.0f;
+  const float2 *pml = reinterpret_cast<const float2 *>(
+      a.part + 2 * static_cast<int64_t>(blocks) * ROWS * D);
+  float top = -INFINITY, sum = 0.0f;
   float4 val = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (int c = first + share; c <= last; c += SPLIT) {
-    const int64_t at = piece(c);
-    const float by = ex2_approx(pml[2 * at] - base);
-    const float4 v = *reinterpret_cast<const float4 *>(a.part + at * D + 4 * lane);
-    sum += by * pml[2 * at + 1];
-    val.x += by * v.x;
-    val.y += by * v.y;
-    val.z += by * v.z;
-    val.w += by * v.w;
+  auto add = [&](float m, float l, float4 v) {
+    const float now = fmaxf(top, m);
+    const float base = now == -INFINITY ? 0.0f : now;
+    const float x = ex2_approx(top - base), y = ex2_approx(m - base);
+    sum = sum * x + l * y;
+    val.x = val.x * x + v.x * y;
+    val.y = val.y * x + v.y * y;
+    val.z = val.z * x + v.z * y;
+    val.w = val.w * x + v.w * y;
+    top = now;
+  };
+  for (int c0 = first + share; c0 <= last; c0 += RUN * SPLIT) {
+    float2 ml[RUN];
+    float4 v[RUN];
+#pragma unroll
+    for (int x = 0; x < RUN; ++x) {
+      const int c = min(c0 + x * SPLIT, last);
+      // piece of block c: the first block's may be its second one
+      const int64_t at =
+          (2 * static_cast<int64_t>(c) + (c == first ? (w.z & 1) : 0)) * ROWS + row;
+      ml[x] = pml[at];
+      v[x] = *reinterpret_cast<const float4 *>(a.part + at * D + 4 * lane);
+    }
+#pragma unroll
+    for (int x = 0; x < RUN; ++x)
+      if (c0 + x * SPLIT <= last) add(ml[x].x, ml[x].y, v[x]);
   }
   s_val[share][row][lane] = val;
-  if (lane == 0) s_sum[share][row] = sum;
+  if (lane == 0) s_sum[share][row] = make_float2(top, sum);
   __syncthreads();
   if (share != 0 || row >= rows) return;
 #pragma unroll
-  for (int x = 1; x < SPLIT; ++x) {
-    const float4 v = s_val[x][row][lane];
-    sum += s_sum[x][row];
-    val.x += v.x;
-    val.y += v.y;
-    val.z += v.z;
-    val.w += v.w;
-  }
+  for (int x = 1; x < SPLIT; ++x)
+    add(s_sum[x][row].x, s_sum[x][row].y, s_val[x][row][lane]);
   const float out_by = a.s_out ? __ldg(a.s_v) / __ldg(a.s_out) : __ldg(a.s_v);
   const float by = sum != 0.0f ? out_by / sum : 0.0f;
   const int i = (row0 + row) / a.group;
