@@ -64,6 +64,7 @@ struct KvAttnArgs {
   const float *s_v;
   float scale;
   int causal;
+  int splits;    // of fp4_kv_tiles_kernel's tokens
   int few_rows;  // requests of more rows (tokens x group) are fp4_kv_tiles_kernel's
   const float *s_out;  // null: BF16 output
   void *out;

@@ -23,6 +23,8 @@
 // for 2 chunks of 2048 rows, and 280 with the softmax left out.)  A row's maximum
 // is moved, and its sums in TMEM scaled, only when a score exceeds it by 2^10
 // (FP16 weights have that room).
+// Where the row blocks do not fill the GPU, `splits` blocks share one's tokens
+// and leave partial sums, which fp4_kv_tiles_merge_kernel adds in order.
 // Bound, for 256 rows and 64 tokens: 2 x (390 + 260) cycles of the tensor pipe
 // (D = 128; the first product, N = 64, is held by the reads of Q) beside 1024 of
 // the special function unit (one exponential a score, 16 a cycle).
@@ -34,6 +36,7 @@
 namespace fp8ws {
 
 constexpr int kKvTileRows = 256;
+constexpr int kKvTileSlots = 148;  // partial sums of 256 rows at most
 constexpr int kKvTileThreads = 512;
 constexpr int kKvChunkStrips = kKvChunk / kStripTokens;
 constexpr int kKvRawSlots = 3;  // chunks of raw strips
@@ -197,6 +200,8 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
   }
   pdl_launch_dependents();
   pdl_wait();
+  const int item = static_cast<int>(blockIdx.x) / a.splits;
+  const int split = static_cast<int>(blockIdx.x) - item * a.splits;
   if (warp == 0) {  // this block's request
     int64_t before = 0;
     int found = -1, local = 0;
@@ -209,12 +214,11 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
         const int64_t m = __shfl_up_sync(0xFFFFFFFFu, n, d);
         if (lane >= d) n += m;
       }
-      const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + n > blockIdx.x);
+      const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + n > item);
       if (past) {
         const int src = __ffs(past) - 1;
         found = b0 + src;
-        local = static_cast<int>(blockIdx.x -
-                                 (before + __shfl_sync(0xFFFFFFFFu, n - mine, src)));
+        local = static_cast<int>(item - (before + __shfl_sync(0xFFFFFFFFu, n - mine, src)));
       }
       before += __shfl_sync(0xFFFFFFFFu, n, 31);
     }
@@ -229,6 +233,7 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
   const uint32_t tmem = tmem_slot;
   const int b = s_item[0];
   if (b < 0) {  // more blocks than work
+    if (a.splits > 1 && split == 0 && threadIdx.x == 0) a.meta[item] = make_int4(-1, 0, 0, 0);
     __syncthreads();
     if (warp == 1) tmem_dealloc(tmem, 512);
     return;
@@ -243,7 +248,13 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
   const int row_tiles = rows > 128 ? 2 : 1;
   // tokens that some row of the block sees, and that all of them see
   const int most = kv_limit(req, (row0 + rows - 1) / a.group, a.causal);
-  const int chunks = (most + kKvChunk - 1) / kKvChunk;
+  // this block's chunks of them
+  const int all_chunks = (most + kKvChunk - 1) / kKvChunk;
+  const int per_split = (all_chunks + a.splits - 1) / a.splits;
+  const int chunk0 = min(split * per_split, all_chunks);
+  const int chunks = min(per_split, all_chunks - chunk0);
+  if (a.splits > 1 && split == 0 && threadIdx.x == 0)
+    a.meta[item] = make_int4(b, head, row0, rows);
 
   // A wait of the whole warp, and what follows when it runs out.
   auto wait = [&](uint64_t *bar, int n) {
@@ -271,18 +282,19 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     const int32_t *table = a.table + static_cast<int64_t>(b) * a.width;
-    const int strips = (most + kStripTokens - 1) / kStripTokens;
+    const int strips = min((most + kStripTokens - 1) / kStripTokens,
+                           (chunk0 + chunks) * kKvChunkStrips);
     auto page_of = [&](int strip) {
       return lane < kKvChunkStrips && strip < strips
                  ? table[(strip * kStripTokens) >> a.cache.page_shift]
                  : -1;
     };
-    int page = page_of(lane);
+    int page = page_of(chunk0 * kKvChunkStrips + lane);
     int i = 0;
     for (; i < chunks; ++i) {
       const int slot = i % kKvRawSlots;
       if (!wait(&raw_empty[slot], i / kKvRawSlots + 1)) break;
-      const int strip = i * kKvChunkStrips + lane;
+      const int strip = (chunk0 + i) * kKvChunkStrips + lane;
       const bool there = page >= 0 && page < a.cache.pages;
       const uint32_t mask = __ballot_sync(0xFFFFFFFFu, there);
       if (lane == 0) {
@@ -362,48 +374,38 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
     finish(leader, 1);
   } else if (warp >= 12) {
     // ------------------------------------------------------------ codes to FP16
-    const int w = warp - 12;
+    const int w = warp - 12;  // this warp's strip of a chunk
     bool ok = true;
-    // this warp's strip of a chunk: 16 tokens of K or V
-    auto convert = [&](const uint8_t *strip, uint8_t *tile, bool is_v, int tok0, bool gone) {
-      constexpr int LANES = D / 32;      // lanes of a row, 32 elements (16 bytes of codes) each
-      constexpr int ROWS = 32 / LANES;   // rows of a round
-      const int part = lane % LANES;
+    constexpr int LANES = D / 32;              // lanes of a row, 32 elements (16 bytes of codes) each
+    constexpr int ROWS = 32 / LANES;           // rows of a round
+    constexpr int ROUNDS = kStripTokens / ROWS;
+    const int part = lane % LANES;
+    // 32 codes and their two scales to FP16, to a row of an FP16 tile
+    auto convert = [&](const uint4 &codes, uint32_t scales, uint8_t *tile, int row) {
+      const uint32_t sh = cvt_f16_e4m3x2(scales);
+      const __half2 s = *reinterpret_cast<const __half2 *>(&sh);
+      const __half2 s0 = __low2half2(s), s1 = __high2half2(s);
+      uint32_t h[4][4];
+      cvt_f16_e2m1x8(codes.x, h[0]);
+      cvt_f16_e2m1x8(codes.y, h[1]);
+      cvt_f16_e2m1x8(codes.z, h[2]);
+      cvt_f16_e2m1x8(codes.w, h[3]);
 #pragma unroll
-      for (int x = 0; x < kStripTokens / ROWS; ++x) {
-        const int in = x * ROWS + lane / LANES;
-        const int row = w * kStripTokens + in;
-        const uint4 codes = *reinterpret_cast<const uint4 *>(strip + (is_v ? strip_v(D) : 0) +
-                                                             in * (D / 2) + part * 16);
-        uint32_t sc = *reinterpret_cast<const uint16_t *>(
-            strip + (is_v ? strip_vs(D) : strip_ks(D)) + in * (D / 16) + part * 2);
-        // V of tokens that are not there has to be finite: rows weigh it with 0
-        if (is_v && (gone || tok0 + row >= req.kv)) sc = 0;
-        const uint32_t sh = cvt_f16_e4m3x2(sc);
-        const __half2 s = *reinterpret_cast<const __half2 *>(&sh);
-        const __half2 s0 = __low2half2(s), s1 = __high2half2(s);
-        uint32_t h[4][4];
-        cvt_f16_e2m1x8(codes.x, h[0]);
-        cvt_f16_e2m1x8(codes.y, h[1]);
-        cvt_f16_e2m1x8(codes.z, h[2]);
-        cvt_f16_e2m1x8(codes.w, h[3]);
+      for (int y = 0; y < 4; ++y) {
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
+        for (int z = 0; z < 4; ++z) h[y][z] = scaled(h[y][z], y < 2 ? s0 : s1);
+      }
+      // 16-byte units 4 (part % 2) + y of the row's 128 bytes in atom part / 2,
+      // swizzled; the second atom's lanes go in another order, which keeps the
+      // eight lanes of a store phase on eight different units
+      uint8_t *to = tile + part / 2 * C::KV_ATOM + row * 128;
+      const int turn = part / 2 * 2;
 #pragma unroll
-          for (int z = 0; z < 4; ++z) h[y][z] = scaled(h[y][z], y < 2 ? s0 : s1);
-        }
-        // 16-byte units 4 (part % 2) + y of the row's 128 bytes in atom part / 2,
-        // swizzled; the second atom's lanes go in another order, which keeps
-        // the eight lanes of a store phase on eight different units
-        uint8_t *to = tile + part / 2 * C::KV_ATOM + row * 128;
-        const int turn = part / 2 * 2;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int unit = part % 2 * 4 + (y ^ turn);
-          const uint4 v = turn ? make_uint4(h[y ^ 2][0], h[y ^ 2][1], h[y ^ 2][2], h[y ^ 2][3])
-                               : make_uint4(h[y][0], h[y][1], h[y][2], h[y][3]);
-          *reinterpret_cast<uint4 *>(to + ((unit ^ (row & 7)) << 4)) = v;
-        }
+      for (int y = 0; y < 4; ++y) {
+        const int unit = part % 2 * 4 + (y ^ turn);
+        const uint4 v = turn ? make_uint4(h[y ^ 2][0], h[y ^ 2][1], h[y ^ 2][2], h[y ^ 2][3])
+                             : make_uint4(h[y][0], h[y][1], h[y][2], h[y][3]);
+        *reinterpret_cast<uint4 *>(to + ((unit ^ (row & 7)) << 4)) = v;
       }
     };
     for (int i = 0; i < chunks && ok; ++i) {
@@ -412,21 +414,34 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
       ok = wait(&raw_full[slot], i / kKvRawSlots);
       if (!ok) break;
       const bool gone = missing[i % kKvMasks] >> w & 1u;
-      // the products with what the buffer held before are done
-      ok = wait(&k_empty[buf], use + 1);
-      if (!ok) break;
-      convert(strip, sK + buf * C::KV_TILE, false, i * kKvChunk, gone);
-      fence_async_shared();
+      uint4 kc[ROUNDS], vc[ROUNDS];
+      uint32_t ks[ROUNDS], vs[ROUNDS];
+#pragma unroll
+      for (int x = 0; x < ROUNDS; ++x) {
+        const int in = x * ROWS + lane / LANES;
+        kc[x] = *reinterpret_cast<const uint4 *>(strip + in * (D / 2) + part * 16);
+        vc[x] = *reinterpret_cast<const uint4 *>(strip + strip_v(D) + in * (D / 2) + part * 16);
+        ks[x] = *reinterpret_cast<const uint16_t *>(strip + strip_ks(D) + in * (D / 16) + part * 2);
+        vs[x] = *reinterpret_cast<const uint16_t *>(strip + strip_vs(D) + in * (D / 16) + part * 2);
+        // V of tokens that are not there has to be finite: rows weigh it with 0
+        if (gone || (chunk0 + i) * kKvChunk + w * kStripTokens + in >= req.kv) vs[x] = 0;
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&k_full[buf]);
-      ok = wait(&v_empty[buf], use + 1);
+      if (lane == 0) mbar_arrive(&raw_empty[slot]);
+      // the products with what the buffers held before are done
+      ok = wait(&k_empty[buf], use + 1) && wait(&v_empty[buf], use + 1);
       if (!ok) break;
-      convert(strip, sV + buf * C::KV_TILE, true, i * kKvChunk, gone);
+#pragma unroll
+      for (int x = 0; x < ROUNDS; ++x)
+        convert(kc[x], ks[x], sK + buf * C::KV_TILE, w * kStripTokens + x * ROWS + lane / LANES);
+#pragma unroll
+      for (int x = 0; x < ROUNDS; ++x)
+        convert(vc[x], vs[x], sV + buf * C::KV_TILE, w * kStripTokens + x * ROWS + lane / LANES);
       fence_async_shared();
       __syncwarp();
       if (lane == 0) {
+        mbar_arrive(&k_full[buf]);
         mbar_arrive(&v_full[buf]);
-        mbar_arrive(&raw_empty[slot]);
       }
     }
   } else if (warp >= 4) {
@@ -481,7 +496,7 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
       uint32_t s0[32], s1[32];  // the scores of 32 tokens each
       tmem_ld_32x32b_x32(t_s, s0);
       tmem_ld_32x32b_x32(t_s + 32, s1);
-      const int tok0 = i * kKvChunk;
+      const int tok0 = (chunk0 + i) * kKvChunk;
       const uint32_t gone = missing[i % kKvMasks];
       const bool edge = __any_sync(0xFFFFFFFFu, tok0 + kKvChunk > lim) || gone != 0;
       tmem_ld_wait();
@@ -554,7 +569,22 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
       ok = wait(&pv_done[tile][(chunks - 1) & 1], (chunks - 1) >> 1);
       tc_fence_after();
     }
-    if (used && ok) {
+    if (used && ok && a.splits > 1) {  // sums as they are
+      const int64_t slot = static_cast<int64_t>(blockIdx.x) * kKvTileRows + r;
+#pragma unroll 1
+      for (int col = 0; chunks > 0 && col < D; col += 32) {
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(t_o + col, o);
+        tmem_ld_wait();
+        if (!live) continue;
+#pragma unroll
+        for (int x = 0; x < 32; x += 4)
+          *reinterpret_cast<uint4 *>(a.part + slot * D + col + x) =
+              make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+      }
+      float *ml = a.part + static_cast<int64_t>(kKvTileSlots) * kKvTileRows * D;
+      if (live) *reinterpret_cast<float2 *>(ml + 2 * slot) = make_float2(-neg_m, l);
+    } else if (used && ok) {
       const float s_v = a.s_out ? __ldg(a.s_v) / __ldg(a.s_out) : __ldg(a.s_v);
       const float by = l != 0.0f ? s_v / l : 0.0f;
 #pragma unroll 1
@@ -596,6 +626,54 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// Adds the partial sums of a row block's splits, in order: 8 rows a block (16
+// where D = 64), 4 of a row's values a thread.
+constexpr int kKvTileMergeThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kKvTileMergeThreads)
+    fp4_kv_tiles_merge_kernel(const KvAttnArgs a) {
+  constexpr int LANES = D / 4;
+  constexpr int ROWS = kKvTileMergeThreads / LANES;
+  constexpr int BLOCKS = kKvTileRows / ROWS;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int item = static_cast<int>(blockIdx.x) / BLOCKS;
+  const int4 w = a.meta[item];
+  const int r = static_cast<int>(blockIdx.x) % BLOCKS * ROWS + static_cast<int>(threadIdx.x) / LANES;
+  if (w.x < 0 || r >= w.w) return;
+  const int lane = threadIdx.x % LANES;
+  const float2 *ml = reinterpret_cast<const float2 *>(
+      a.part + static_cast<int64_t>(kKvTileSlots) * kKvTileRows * D);
+  float top = -INFINITY, sum = 0.0f;
+  float4 val = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s) {
+    const int64_t slot = static_cast<int64_t>(item * a.splits + s) * kKvTileRows + r;
+    const float2 p = ml[slot];
+    const float4 v = *reinterpret_cast<const float4 *>(a.part + slot * D + 4 * lane);
+    // nothing seen there, and nothing written where it had no chunk; but a NaN sum counts
+    if (p.x == -INFINITY && p.y == 0.0f) continue;
+    const float now = fmaxf(top, p.x);
+    const float base = now == -INFINITY ? 0.0f : now;
+    const float x = ex2_approx(top - base), y = p.x == -INFINITY ? 1.0f : ex2_approx(p.x - base);
+    sum = sum * x + p.y * y;
+    val.x = val.x * x + v.x * y;
+    val.y = val.y * x + v.y * y;
+    val.z = val.z * x + v.z * y;
+    val.w = val.w * x + v.w * y;
+    top = now;
+  }
+  const KvRequest req = kv_request(a, w.x);
+  const int i = (w.z + r) / a.group;
+  const int64_t at = (static_cast<int64_t>(req.q0 + i) * a.cache.heads + w.y) * a.group +
+                     (w.z + r) % a.group;
+  const float out_by = a.s_out ? __ldg(a.s_v) / __ldg(a.s_out) : __ldg(a.s_v);
+  const float by = sum != 0.0f ? out_by / sum : 0.0f;
+  kv_store4(a, at * D + 4 * lane, make_float4(val.x * by, val.y * by, val.z * by, val.w * by));
+  if (a.lse && lane == 0) a.lse[at] = (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 }  // namespace fp8ws

@@ -1084,12 +1084,27 @@ int launch_kv_rows(DeviceInfo *d, KvAttnArgs a, cudaStream_t st) {
   return launch_status();
 }
 
-// Requests of up to this many rows (tokens x query heads of a K/V head) go to
-// fp4_kv_rows_kernel, of more to fp4_kv_tiles_kernel.
-constexpr int kKvFewRows = 32;
+// Which kernel takes a request's rows (tokens x query heads of a K/V head).
+// Timed on B200 (32 requests of 1024 tokens, 8 heads of 128): 16 rows 27 us by
+// fp4_kv_rows_kernel and 44 by fp4_kv_tiles_kernel, 32 rows 39 and 44, 48 rows 50
+// and 44, 128 rows 109 and 45; 64-wide heads cross between 48 and 64 rows.  With a
+// handful of 256-row blocks in all, the GPU is idle even with their splits (one
+// head, 8192 tokens: 128 rows 21.4 and 21.5 us, 256 rows 20.9 and 28.0).
+constexpr int kKvFewRows = 40;
+constexpr int kKvFewItems = 4;
+// Chunks of a split at least, by the longest request that the tables can hold.
+constexpr int64_t kKvSplitChunks = 8;
+
+// 256-row blocks there can be: one begun by each request of more than few_rows
+// rows beside the full ones.
+int64_t kv_tile_blocks(const KvAttnArgs &a) {
+  const int64_t rows = static_cast<int64_t>(a.total_q) * a.group;
+  const int64_t begun = rows / (a.few_rows + 1);
+  return a.cache.heads * (rows / kKvTileRows + (begun < a.batch ? begun : a.batch));
+}
 
 template <int D, int BIT>
-int launch_kv_tiles(DeviceInfo *d, const KvAttnArgs &a, cudaStream_t st) {
+int launch_kv_tiles(DeviceInfo *d, KvAttnArgs a, cudaStream_t st) {
   using C = KvTilesCfg<D>;
   auto kern = fp4_kv_tiles_kernel<D>;
   int rc = once_per_device(d, BIT, [&] {
@@ -1099,18 +1114,34 @@ int launch_kv_tiles(DeviceInfo *d, const KvAttnArgs &a, cudaStream_t st) {
                : FP8WS_ERR_CUDA;
   });
   if (rc) return rc;
-  // 256-row blocks there can be: one begun by each request of more than
-  // few_rows rows beside the full ones
-  const int64_t rows = static_cast<int64_t>(a.total_q) * a.group;
-  const int64_t begun = rows / (a.few_rows + 1);
-  const int64_t blocks = a.cache.heads * (rows / kKvTileRows + (begun < a.batch ? begun : a.batch));
+  const int64_t blocks = kv_tile_blocks(a);
   if (blocks == 0) return FP8WS_OK;
-  if (launch_ex(kern, dim3(static_cast<unsigned>(blocks)), dim3(kKvTileThreads), C::SMEM, st, 1, a,
-                kWaitLimitNs) != cudaSuccess)
+  const int64_t places = d->sms < kKvTileSlots ? d->sms : kKvTileSlots;
+  const int64_t longest = (a.width << a.cache.page_shift) / (kKvSplitChunks * kKvChunk);
+  int64_t splits = places / blocks;
+  if (splits > longest) splits = longest;
+  a.splits = splits > 1 ? static_cast<int>(splits) : 1;
+  if (launch_ex(kern, dim3(static_cast<unsigned>(blocks * a.splits)), dim3(kKvTileThreads), C::SMEM,
+                st, 1, a, kWaitLimitNs) != cudaSuccess)
     return FP8WS_ERR_CUDA;
   log_launch(kKindKvAttention, a.q, a.cache.data, a.out);
+  if (a.splits > 1) {
+    constexpr int per_item = kKvTileRows / (kKvTileMergeThreads / (D / 4));
+    if (launch_ex(fp4_kv_tiles_merge_kernel<D>, dim3(static_cast<unsigned>(blocks * per_item)),
+                  dim3(kKvTileMergeThreads), 0, st, 1, a) != cudaSuccess)
+      return FP8WS_ERR_CUDA;
+    log_launch(kKindKvAttention, a.part, nullptr, a.out);
+  }
   return launch_status();
 }
+
+// Partial sums: two pieces per block of up to 16 rows x 128 (few rows), or
+// kKvTileSlots of 256 rows x 128 (many rows), with their maxima and sums; then
+// the merge records.
+constexpr size_t kKvPartFloats =
+    static_cast<size_t>(kKvTileSlots) * kKvTileRows * (128 + 2);
+static_assert(kKvPartFloats >= static_cast<size_t>(2 * kKvMaxBlocks) * 16 * (128 + 2), "workspace");
+static_assert(kKvMaxBlocks >= kKvTileSlots, "merge records");
 
 }  // namespace
 }  // namespace fp8ws
@@ -1873,11 +1904,8 @@ int fp4_kv_gather(const uint8_t *cache, int64_t num_pages, int page_size, int64_
   return launch_status();
 }
 
-// Partial sums of two pieces per block of up to 16 rows x 128, their maxima and
-// sums, and the blocks' merge records.
 size_t fp4_kv_attention_workspace(void) {
-  return round256(static_cast<size_t>(2 * kKvMaxBlocks) * 16 * (128 + 2) * sizeof(float)) +
-         round256(kKvMaxBlocks * sizeof(int4));
+  return round256(kKvPartFloats * sizeof(float)) + round256(kKvMaxBlocks * sizeof(int4));
 }
 
 int fp4_kv_attention(const uint16_t *q, int64_t total_q, int64_t q_heads, int64_t batch,
@@ -1908,22 +1936,22 @@ int fp4_kv_attention(const uint16_t *q, int64_t total_q, int64_t q_heads, int64_
   rc = device_info(&d);
   if (rc) return rc;
   if (total_q == 0 || batch == 0 || max_q == 0) return FP8WS_OK;
-  const size_t part_bytes =
-      round256(static_cast<size_t>(2 * kKvMaxBlocks) * 16 * (128 + 2) * sizeof(float));
+  const size_t part_bytes = round256(kKvPartFloats * sizeof(float));
   KvAttnArgs a{q, static_cast<int>(total_q), static_cast<int>(batch),
                      static_cast<int>(q_heads / kv_heads), cu_q, kv_lens, block_table, table_width,
                      KvCache{const_cast<uint8_t *>(cache), num_pages, static_cast<int>(kv_heads),
                              page_shift(page_size)},
-                     s_k, s_v, scale, causal ? 1 : 0, kKvFewRows, s_out, out, lse,
+                     s_k, s_v, scale, causal ? 1 : 0, 1, kKvFewRows, s_out, out, lse,
                      static_cast<float *>(workspace),
                      reinterpret_cast<int4 *>(static_cast<uint8_t *>(workspace) + part_bytes)};
   const int64_t most = max_q * (q_heads / kv_heads);  // rows of a request
   cudaStream_t st = as_stream(stream);
-  if (most > kKvFewRows) {
+  if (batch == 1) a.few_rows = 0;  // one request, one kernel
+  if (most > kKvFewRows && kv_tile_blocks(a) > kKvFewItems) {
     rc = head_dim == 128 ? launch_kv_tiles<128, 40>(d, a, st) : launch_kv_tiles<64, 41>(d, a, st);
-    if (rc) return rc;
+    if (rc || batch == 1) return rc;
   } else {
-    a.few_rows = INT_MAX;  // should a request have more than max_q rows after all
+    a.few_rows = INT_MAX;  // all of them, should one have more than max_q rows, too
   }
   if (head_dim == 128)
     return most <= 8 ? launch_kv_rows<128, 1, 32>(d, a, st) : launch_kv_rows<128, 2, 33>(d, a, st);
