@@ -142,6 +142,38 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// Two fp32 at a time: half the issue slots of the softmax's multiply-adds and sums.
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  return pair(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  uint32_t lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;"
+      : "=f"(r)
+      : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  return r;
+}
+
 // 256-row blocks of request b over all heads, 0 for a request whose rows the
 // other kernel takes.
 __device__ __forceinline__ int64_t kv_tile_items(const KvAttnArgs &a, int b) {
@@ -513,10 +545,8 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
       float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
       for (int x = 0; x < 32; x += 2) {
-        tops[0] = fmaxf(tops[0], __uint_as_float(s0[x]));
-        tops[1] = fmaxf(tops[1], __uint_as_float(s0[x + 1]));
-        tops[2] = fmaxf(tops[2], __uint_as_float(s1[x]));
-        tops[3] = fmaxf(tops[3], __uint_as_float(s1[x + 1]));
+        tops[x / 2 % 2] = max3(tops[x / 2 % 2], s0[x], s0[x + 1]);
+        tops[2 + x / 2 % 2] = max3(tops[2 + x / 2 % 2], s1[x], s1[x + 1]);
       }
       const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
       const float now = top == -INFINITY ? -INFINITY : top * c;
@@ -543,23 +573,23 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
       }
       // a row that has seen nothing yet has no maximum: any, for weights of 0
       const float shift = neg_m == INFINITY ? 0.0f : neg_m;
-      float sums[2] = {0.0f, 0.0f};
+      const uint64_t c2 = pair(c, c), shift2 = pair(shift, shift);
+      uint64_t sums = pair(0.0f, 0.0f);
       // weights, rounded to FP16 (2^-11 of each) for the second product
       auto weigh = [&](const uint32_t (&s)[32], uint32_t col) {
         uint32_t p[16];
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
-          const float e0 = ex2_approx(fmaf(__uint_as_float(s[2 * x]), c, shift));
-          const float e1 = ex2_approx(fmaf(__uint_as_float(s[2 * x + 1]), c, shift));
-          sums[0] += e0;
-          sums[1] += e1;
+          const float2 v = unpair(fma2(pair(s[2 * x], s[2 * x + 1]), c2, shift2));
+          const float e0 = ex2_approx(v.x), e1 = ex2_approx(v.y);
+          sums = add2(sums, pair(e0, e1));
           p[x] = pack_f16(e0, e1);
         }
         tmem_st_32x32b_x16(col, p);
       };
       weigh(s0, t_s);
       weigh(s1, t_s + 16);
-      l += sums[0] + sums[1];
+      l += unpair(sums).x + unpair(sums).y;
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
