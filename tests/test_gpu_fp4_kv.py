@@ -231,6 +231,27 @@ def test_prompts(q_len, kv, causal, dim, group):
     attend([q_len], [kv], 2, group, dim, 64, causal, seed=q_len)
 
 
+@pytest.mark.parametrize("q_len", [39, 40, 41, 128, 129, 256, 257])
+@pytest.mark.parametrize("batch", [1, 3])
+def test_rows_where_the_kernel_changes(q_len, batch):
+    """The borders in rows between the two kernels and between row tiles; one
+    request's row blocks share the GPU by splits of its tokens."""
+    attend([q_len] * batch, [1500 - 700 * b for b in range(batch)], 1, 1, 128, 32, True, seed=q_len)
+
+
+@pytest.mark.parametrize("kv", [63, 64, 65, 600, 20000])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_splits_of_the_tokens(kv, dim):
+    """Five row blocks in all: the splits' ranges end anywhere, some are empty."""
+    attend([1270], [kv], 1, 1, dim, 64, False, seed=kv)
+
+
+def test_more_rows_than_the_table_has_requests_for():
+    """max_q above every request's rows (a captured graph's bound)."""
+    attend([3, 1, 50], [90, 7, 50], 2, 2, 64, 16, True, max_q=4096)
+    attend([3], [90], 2, 2, 64, 16, True, max_q=4096)
+
+
 @pytest.mark.parametrize("q_len", [1, 40])
 def test_rows_without_tokens(q_len):
     q = [q_len, q_len, q_len]

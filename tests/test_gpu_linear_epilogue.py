@@ -83,6 +83,19 @@ def test_against_the_formula(M, N, K, bias, act, residual, fp8):
     check(y, v, a, K, s_out)
 
 
+@pytest.mark.parametrize("M", [31, 32, 33, 63, 64, 65, 100, 127, 128, 129])
+@pytest.mark.parametrize("N,K", [(528, 2048), (96, 4112), (6000, 384)])
+def test_row_counts_where_the_kernel_changes(M, N, K):
+    """The kernels' borders in rows, each with K split over a cluster in
+    several ways (its last range short), and the same bits again."""
+    xq, wq, b, r = make(M, N, K, M)
+    args = (xq, wq, one(S_IN), one(S_W), b, "gelu", r)
+    y = fw.fp8_linear_epilogue(*args)
+    v, a = formula(xq, wq, float(one(S_IN).double() * one(S_W).double()), b, "gelu", r)
+    check(y, v, a, K)
+    assert torch.equal(fw.fp8_linear_epilogue(*args), y)
+
+
 @pytest.mark.parametrize("N", [8, 24, 1000])
 def test_widths_of_eight(N):
     xq, wq, b, r = make(70, N, 64, N)
@@ -102,13 +115,12 @@ def test_plain_is_fp8_linear_static(M):
     assert ((y.double() - z.double()).abs() <= 2.0 ** -7 * z.double().abs() + 2 * 1040 * 2.0 ** -21 * a).all()
 
 
-@pytest.mark.parametrize("M", [5, 33, 600])
+@pytest.mark.parametrize("M", [5, 33, 64, 100, 600])
 def test_residual_in_place(M):
     xq, wq, b, r = make(M, 528, 256, M)
     want = fw.fp8_linear_epilogue(xq, wq, one(S_IN), one(S_W), b, "none", r)
     got = r.clone()
-    for _ in range(1):
-        fw.fp8_linear_epilogue(xq, wq, one(S_IN), one(S_W), b, "none", got, out=got)
+    fw.fp8_linear_epilogue(xq, wq, one(S_IN), one(S_W), b, "none", got, out=got)
     assert torch.equal(got, want)
 
 
