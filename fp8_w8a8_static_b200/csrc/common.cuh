@@ -127,21 +127,8 @@ __device__ __forceinline__ bool mbar_wait_bounded_warp(uint64_t *bar, uint32_t p
   }
 }
 
-// The same waits for loops that wait often and briefly: the clock, a slow read,
+// The same wait for loops that wait often and briefly: the clock, a slow read,
 // is looked at only after 256 polls.
-__device__ __forceinline__ bool mbar_wait_polled(uint64_t *bar, uint32_t parity,
-                                                 volatile int *abort, uint64_t limit_ns) {
-  uint64_t t0 = 0;
-  for (uint32_t spins = 1;; ++spins) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((spins & 255u) == 0) {
-      const uint64_t now = global_timer_ns();
-      if (t0 == 0) t0 = now;
-      if (*abort || now - t0 > limit_ns) return false;
-    }
-  }
-}
-
 __device__ __forceinline__ bool mbar_wait_polled_warp(uint64_t *bar, uint32_t parity,
                                                       volatile int *abort, uint64_t limit_ns) {
   uint64_t t0 = 0;

@@ -23,7 +23,13 @@
 // of the whole batch form one sequence, and block c takes the c-th of equal
 // ranges, whatever the lengths.  A (request, row tile, head) that ends up in
 // several ranges leaves partial sums, which fp4_kv_merge_kernel adds in range
-// order (no atomics: the result does not depend on timing).
+// order (no atomics: the result does not depend on timing).  Measured: 6 requests
+// of 30 to 131 thousand tokens, 32 query heads on 4 K/V heads of 128: 67 us (299
+// MB, 4.5 TB/s; 74 before the masks went to the edges, 92 with one warp filling a
+// ring for the other four); 48 requests of 17 to 6000 tokens, 24 heads on 8: 44 us
+// (3.9 TB/s); one of 1001 tokens: 9.5 us.  Some 10 us are the search for the
+// range, the first copies and the merge; beside the stream it is the conversions
+// (two cycles of the ALU pipe each) that fill the issue slots.
 #pragma once
 
 #include "common.cuh"

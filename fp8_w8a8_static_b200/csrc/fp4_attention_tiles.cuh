@@ -10,24 +10,28 @@
 //                 deep.  K is read K-major, V MN-major (its inner index, the
 //                 token, is the row), so both are written the same way and
 //                 nothing is transposed.
-//   warp 1        issues the MMAs: S = Q_t K^T (M = 128, N = 64) into TMEM,
-//                 O_t += P_t V with P_t read from TMEM, in S's place
+//   warp 1        issues the first product, S = Q_t K^T (M = 128, N = 64) into TMEM
+//   warp 2        issues the second, O_t += P_t V, P_t read from TMEM, in S's place
 //   warps 4..11   softmax: four warps a row tile, a thread a row, so the maximum
 //                 and the sum need no exchange; a chunk's scores stay in
 //                 registers from the search for the maximum to the weights.
 // Each row tile has two score buffers: while the softmax is on one chunk, the
-// next one's scores are computed, and a chunk's scores are asked for one event
-// after the products that free their buffer, when the other row tile's are in
-// between, so that the issuing thread hardly waits.  (Chunks of 128 tokens with
-// one buffer a row tile, products and scores taking turns: 315 against 240 us
-// for 2 chunks of 2048 rows, and 280 with the softmax left out.)  A row's maximum
-// is moved, and its sums in TMEM scaled, only when a score exceeds it by 2^10
-// (FP16 weights have that room).
+// next one's scores are computed.  A row's maximum is moved, and its sums in TMEM
+// scaled, only when a score exceeds it by 2^10 (FP16 weights have that room).
 // Where the row blocks do not fill the GPU, `splits` blocks share one's tokens
 // and leave partial sums, which fp4_kv_tiles_merge_kernel adds in order.
 // Bound, for 256 rows and 64 tokens: 2 x (390 + 260) cycles of the tensor pipe
 // (D = 128; the first product, N = 64, is held by the reads of Q) beside 1024 of
-// the special function unit (one exponential a score, 16 a cycle).
+// the special function unit (one exponential a score, 16 a cycle).  Measured
+// (24 query heads on 8 K/V heads of 128, 2 x 2048 rows over 3000 to 8192 tokens):
+// 278 us, about 2200 cycles a chunk, the rest being what the warps wait for one
+// another; 45 us for 4096 rows over 1024 tokens, 64-wide heads.
+// On the way, for the first of them: 350 us with chunks of 128 tokens and one score
+// buffer, 315 with half of a chunk's weights handed over at a time, 320 as now but
+// with each MMA issued from one thread's own registers, 283 with the issue
+// warp-uniform, 278 with packed fp32 pairs in the softmax.  Ranges of tokens cut
+// evenly over persistent blocks were slower (300 us): nearly every range then
+// leaves partial sums.
 #pragma once
 
 #include "common.cuh"
@@ -514,7 +518,7 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
       }
       fence_async_shared();
     }
-    asm volatile("bar.sync 1, 288;" ::: "memory");  // with the MMA warp
+    asm volatile("bar.sync 1, 288;" ::: "memory");  // with the warp that reads it
     const bool used = tile < row_tiles;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t t_o = tmem + lanes + C::O_COL + tile * 128;

@@ -97,12 +97,13 @@ __device__ __forceinline__ int64_t strip_offset(const KvCache &c, int64_t slot, 
 // A lane owns the 16 values of a scale, so nothing is exchanged but the NaN
 // ballot: D/16 lanes for a token's K of one head, D/16 for its V.  Bound by the
 // values' bytes (2 read, 0.56 written).  An IEEE division per value would cost
-// more than the stream (26 us for 8191 x 8 x 128 with it), so a code is first
-// bracketed: with r = fl32(1 / by), x fl32(r (1 - 2^-20)) and x fl32(r (1 +
-// 2^-20)) lie on either side of fl32(x / by) (each of their two roundings, and
-// the quotient's, is 2^-24); where both have one code it is the quotient's, and
-// only lanes with a code that differs divide.
-constexpr int kKvUnroll = 1;  // units in flight per lane
+// more than the stream (append and gather of 8191 x 8 x 128: 35 us with it, 24.5
+// without), so a code is first bracketed: with r = fl32(1 / by), x fl32(r (1 -
+// 2^-20)) and x fl32(r (1 + 2^-20)) lie on either side of fl32(x / by) (each of
+// their two roundings, and the quotient's, is 2^-24); where both have one code
+// it is the quotient's, and only lanes with a code that differs divide.  Two or
+// four units of a lane in flight were not faster: the resident blocks have
+// enough loads out.
 
 // Codes of x[8] / by, the IEEE quotient's.  r is 1 / by, 0 to divide at once.
 __device__ __forceinline__ uint32_t quotient_codes(const float (&x)[8], float by, float r) {
@@ -180,42 +181,30 @@ __global__ void __launch_bounds__(kKvThreads)
   const int64_t stride = static_cast<int64_t>(gridDim.x) * UNITS;
   const uint32_t mine = ((1u << LANES) - 1u) << (threadIdx.x % 32 / LANES * LANES);
   const uint16_t *from = is_v ? v : k;
-  // every lane of a warp runs the same number of rounds (the ballots below)
-  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * UNITS; u0 < units;
-       u0 += kKvUnroll * stride) {
-    uint4 w[kKvUnroll][2];
-    int64_t slot[kKvUnroll];
-    int head[kKvUnroll];
-#pragma unroll
-    for (int x = 0; x < kKvUnroll; ++x) {
-      const int64_t u = u0 + x * stride + threadIdx.x / LANES;
-      w[x][0] = w[x][1] = make_uint4(0, 0, 0, 0);
-      slot[x] = -1;
-      head[x] = 0;
-      if (u < units) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(from + u * D) + 2 * part;
-        w[x][0] = ld_stream(src);
-        w[x][1] = ld_stream(src + 1);
-        const int64_t token = units <= INT32_MAX ? static_cast<uint32_t>(u) / c.heads : u / c.heads;
-        head[x] = static_cast<int>(u - token * c.heads);
-        slot[x] = __ldg(slots + token);
-      }
+  // every lane of a warp runs the same number of rounds (the ballot below)
+  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * UNITS; u0 < units; u0 += stride) {
+    const int64_t u = u0 + threadIdx.x / LANES;
+    uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    int64_t slot = -1;
+    int head = 0;
+    if (u < units) {
+      const uint4 *src = reinterpret_cast<const uint4 *>(from + u * D) + 2 * part;
+      w[0] = ld_stream(src);
+      w[1] = ld_stream(src + 1);
+      const int64_t token = units <= INT32_MAX ? static_cast<uint32_t>(u) / c.heads : u / c.heads;
+      head = static_cast<int>(u - token * c.heads);
+      slot = __ldg(slots + token);
     }
-#pragma unroll
-    for (int x = 0; x < kKvUnroll; ++x) {
-      uint32_t scale;
-      bool nan;
-      const uint2 codes = quantize16(w[x], s, s6, scale, nan);
-      const uint32_t nans = __ballot_sync(0xFFFFFFFFu, nan);
-      if (!is_v && (nans & mine)) scale = 0x7Fu;
-      if (slot[x] < 0 || slot[x] >= n_slots) continue;
-      uint8_t *strip = c.data + strip_offset<D>(c, slot[x], head[x]);
-      const int row = static_cast<int>(slot[x] & (kStripTokens - 1));
-      *reinterpret_cast<uint2 *>(strip + (is_v ? strip_v(D) : 0) + row * (D / 2) + part * 8) =
-          codes;
-      strip[(is_v ? strip_vs(D) : strip_ks(D)) + row * (D / 16) + part] =
-          static_cast<uint8_t>(scale);
-    }
+    uint32_t scale;
+    bool nan;
+    const uint2 codes = quantize16(w, s, s6, scale, nan);
+    const uint32_t nans = __ballot_sync(0xFFFFFFFFu, nan);
+    if (!is_v && (nans & mine)) scale = 0x7Fu;
+    if (slot < 0 || slot >= n_slots) continue;
+    uint8_t *strip = c.data + strip_offset<D>(c, slot, head);
+    const int row = static_cast<int>(slot & (kStripTokens - 1));
+    *reinterpret_cast<uint2 *>(strip + (is_v ? strip_v(D) : 0) + row * (D / 2) + part * 8) = codes;
+    strip[(is_v ? strip_vs(D) : strip_ks(D)) + row * (D / 16) + part] = static_cast<uint8_t>(scale);
   }
 }
 
@@ -236,49 +225,36 @@ __global__ void __launch_bounds__(kKvThreads)
   const int64_t n_slots = c.pages << c.page_shift;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * UNITS;
   uint16_t *to = is_v ? v : k;
-  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * UNITS + threadIdx.x / LANES; u0 < units;
-       u0 += kKvUnroll * stride) {
-    uint2 codes[kKvUnroll];
-    uint32_t scale[kKvUnroll];
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * UNITS + threadIdx.x / LANES; u < units;
+       u += stride) {
+    uint2 codes = make_uint2(0, 0);
+    uint32_t scale = 0;  // zeros for a slot outside the cache
+    const int64_t token = units <= INT32_MAX ? static_cast<uint32_t>(u) / c.heads : u / c.heads;
+    const int head = static_cast<int>(u - token * c.heads);
+    const int64_t slot = __ldg(slots + token);
+    if (slot >= 0 && slot < n_slots) {
+      const uint8_t *strip = c.data + strip_offset<D>(c, slot, head);
+      const int row = static_cast<int>(slot & (kStripTokens - 1));
+      codes = *reinterpret_cast<const uint2 *>(strip + (is_v ? strip_v(D) : 0) + row * (D / 2) +
+                                               part * 8);
+      scale = strip[(is_v ? strip_vs(D) : strip_ks(D)) + row * (D / 16) + part];
+    }
+    const float f = e4m3_to_float(scale);
+    uint32_t h[2][4], r[2][4];
+    cvt_f16_e2m1x8(codes.x, h[0]);
+    cvt_f16_e2m1x8(codes.y, h[1]);
 #pragma unroll
-    for (int x = 0; x < kKvUnroll; ++x) {
-      const int64_t u = u0 + x * stride;
-      codes[x] = make_uint2(0, 0);
-      scale[x] = 0;  // zeros for a slot outside the cache
-      if (u < units) {
-        const int64_t token = units <= INT32_MAX ? static_cast<uint32_t>(u) / c.heads : u / c.heads;
-        const int head = static_cast<int>(u - token * c.heads);
-        const int64_t slot = __ldg(slots + token);
-        if (slot >= 0 && slot < n_slots) {
-          const uint8_t *strip = c.data + strip_offset<D>(c, slot, head);
-          const int row = static_cast<int>(slot & (kStripTokens - 1));
-          codes[x] = *reinterpret_cast<const uint2 *>(strip + (is_v ? strip_v(D) : 0) +
-                                                      row * (D / 2) + part * 8);
-          scale[x] = strip[(is_v ? strip_vs(D) : strip_ks(D)) + row * (D / 16) + part];
-        }
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 e = __half22float2(*reinterpret_cast<__half2 *>(&h[y][i]));
+        // code x scale is exact; two roundings, to fp32 and to BF16
+        const __nv_bfloat162 b = __floats2bfloat162_rn((e.x * f) * s, (e.y * f) * s);
+        r[y][i] = *reinterpret_cast<const uint32_t *>(&b);
       }
-    }
-#pragma unroll
-    for (int x = 0; x < kKvUnroll; ++x) {
-      const int64_t u = u0 + x * stride;
-      if (u >= units) break;
-      const float f = e4m3_to_float(scale[x]);
-      uint32_t h[2][4], r[2][4];
-      cvt_f16_e2m1x8(codes[x].x, h[0]);
-      cvt_f16_e2m1x8(codes[x].y, h[1]);
-#pragma unroll
-      for (int y = 0; y < 2; ++y)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 e = __half22float2(*reinterpret_cast<__half2 *>(&h[y][i]));
-          // code x scale is exact; two roundings, to fp32 and to BF16
-          const __nv_bfloat162 b = __floats2bfloat162_rn((e.x * f) * s, (e.y * f) * s);
-          r[y][i] = *reinterpret_cast<const uint32_t *>(&b);
-        }
-      uint4 *dst = reinterpret_cast<uint4 *>(to + u * D) + 2 * part;
-      st_stream(dst, make_uint4(r[0][0], r[0][1], r[0][2], r[0][3]));
-      st_stream(dst + 1, make_uint4(r[1][0], r[1][1], r[1][2], r[1][3]));
-    }
+    uint4 *dst = reinterpret_cast<uint4 *>(to + u * D) + 2 * part;
+    st_stream(dst, make_uint4(r[0][0], r[0][1], r[0][2], r[0][3]));
+    st_stream(dst + 1, make_uint4(r[1][0], r[1][1], r[1][2], r[1][3]));
   }
 }
 
@@ -292,7 +268,8 @@ __global__ void __launch_bounds__(kKvThreads)
 // for prompts).  The row offsets are searched in shared memory where one round
 // covers the batch.  All of it is latency, not bytes: dependent reads and the
 // instructions of a few SMs are what it counts (300 prompts, 80 thousand
-// tokens: 36 us with a full search per slot and one block filling the pages).
+// tokens: 12.9 us, 36 with a full search per slot and one block filling the
+// pages; 32 requests of one token: 3.4 us).
 constexpr int kTableMaxBlocks = 8;  // the portable cluster size
 constexpr int kTableUnroll = 8;     // slots of a thread in flight
 
