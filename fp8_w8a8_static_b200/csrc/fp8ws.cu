@@ -947,13 +947,12 @@ int launch_gemm_epilogue(DeviceInfo *d, const PairProblem &q, int K, const Epilo
   return launch_status();
 }
 
-// Blocks of a cluster that share a 128-row tile's K in fp8_gemm_rows_kernel:
+// Blocks of a cluster that share a tile's K in fp8_gemm_rows_kernel:
 // the most (1, 2, 4, 8) that all get a K step and whose clusters the GPU holds in
 // one go (`resident` by log2 of the cluster's size; of eight blocks, one an SM,
 // that is fewer clusters than an eighth of the SMs: 16 clusters of 8 took 9.3
 // us at N = K = 2048, their last one waiting for a place).
-int rows_split(const std::atomic<int> (&resident)[4], int64_t N, int num_kb) {
-  const int64_t tiles = (N + 127) / 128;
+int rows_split(const std::atomic<int> (&resident)[4], int64_t tiles, int num_kb) {
   int best = 1;
   for (int x = 1; x < 4; ++x) {
     const int s = 1 << x, per = (num_kb + s - 1) / s;
@@ -962,17 +961,20 @@ int rows_split(const std::atomic<int> (&resident)[4], int64_t N, int num_kb) {
   return best;
 }
 
-// fp8_linear_epilogue's kernel by rows.  Up to 64 the weight streams faster
-// through fp8_gemm_rows_kernel for every N and K tried (64 rows, N x K: 10.4
-// against 12.8 us at 8192 x 2048, 7.1 against 11.8 at 2048 x 2048, 10.9 against
-// 26.2 at 2048 x 8192; 17 rows: 8.2 against 30.5, 6.0 against 13.3, 10.0
-// against 26.1).  From 65 to 128 it pays where K is split at least four ways (128 rows:
-// 10.2 against 12.1 us at 2048 x 2048, 14.4 against 26.6 at 2048 x 8192), not
-// where two ways fill the GPU (15.5 against 13.2 at 8192 x 2048) or K is short
-// (10.5 against 7.4 at 704 x 256).
+// fp8_linear_epilogue's kernel.  Up to 64 rows the weight streams faster
+// through fp8_gemm_rows_kernel (64 rows, N x K: 10.4 against 12.8 us at 8192 x
+// 2048, 7.1 against 11.8 at 2048 x 2048, 10.9 against 26.2 at 2048 x 8192; 17
+// rows: 8.2 against 30.5, 6.0 against 13.3, 10.0 against 26.1; but for 33 to 64 rows at K <= 256, 6.2
+// against 5.7 at 704 x 256).  With more it pays
+// where its 128 x 128 tiles are so few that K is split at least four ways, and
+// there are 12 K steps to split (200 rows: 9.9 against 11.0 us at 2048 x 2048,
+// 14.1 against 25.7 at 2048 x 8192, 9.7 against 9.8 at 2048 x 1536; 1000 rows:
+// 10.2 against 10.8 at 512 x 2048), not where two ways fill the GPU (700 rows:
+// 19.9 against 11.6 at 2048 x 2048) or K is short (200 rows: 9.3 against 8.6 at
+// 2048 x 1024, 9.0 against 7.1 at 2048 x 512).
 constexpr int64_t kFewLinearRows = 64;
-constexpr int64_t kFewLinearRowsSplit = 128;
 constexpr int kFewLinearSplit = 4;
+constexpr int kFewLinearSteps = 12;
 
 // *done = false: the rule above leaves this problem to the CTA-pair kernel.
 template <int NTOK, int BIT>
@@ -1006,16 +1008,17 @@ int launch_gemm_rows(DeviceInfo *d, const PairProblem &q, int K, const EpilogueA
   });
   if (rc) return rc;
   const int num_kb = (K + kGemmBK - 1) / kGemmBK;
-  const int split = rows_split(resident, q.N, num_kb);
-  *done = q.M <= kFewLinearRows || split >= kFewLinearSplit;
+  const int row_tiles = (q.M + NTOK - 1) / NTOK;
+  const int64_t tiles = static_cast<int64_t>((q.N + 127) / 128) * row_tiles;
+  const int split = rows_split(resident, tiles, num_kb);
+  *done = q.M <= kFewLinearRows || (split >= kFewLinearSplit && num_kb >= kFewLinearSteps);
   if (!*done) return FP8WS_OK;
   CUtensorMap mw, mx;
   rc = make_map_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.b, q.N, K, kGemmBK, 128, true);
   if (!rc) rc = make_map_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, q.a, q.M, K, kGemmBK, NTOK, true);
   if (rc) return rc;
-  const int tiles = (q.N + 127) / 128;
-  if (launch_ex(kern, dim3(tiles * split), dim3(kRowsThreads), C::SMEM_BYTES, st, split, mw, mx, e,
-                residual, q.out, q.M, q.N, K, (num_kb + split - 1) / split,
+  if (launch_ex(kern, dim3(static_cast<unsigned>(tiles * split)), dim3(kRowsThreads), C::SMEM_BYTES, st, split, mw, mx, e,
+                residual, q.out, q.M, q.N, K, row_tiles, (num_kb + split - 1) / split,
                 kWaitLimitNs) != cudaSuccess)
     return FP8WS_ERR_CUDA;
   log_launch(kKindGemm, q.a, q.b, q.out);
@@ -1793,13 +1796,11 @@ int fp8_linear_epilogue(const uint8_t *xq, const uint8_t *wq, int64_t M, int64_t
   const EpilogueArgs e{s_in, s_w, bias, s_out, act};
   const int k = static_cast<int>(K);
   cudaStream_t st = as_stream(stream);
-  if (M <= kFewLinearRowsSplit) {
-    bool done = false;
-    rc = M <= 32   ? launch_gemm_rows<32, 42>(d, q, k, e, residual, st, &done)
-         : M <= 64 ? launch_gemm_rows<64, 43>(d, q, k, e, residual, st, &done)
-                   : launch_gemm_rows<128, 44>(d, q, k, e, residual, st, &done);
-    if (rc || done) return rc;
-  }
+  bool done = false;
+  rc = M <= 32   ? launch_gemm_rows<32, 42>(d, q, k, e, residual, st, &done)
+       : M <= 64 ? launch_gemm_rows<64, 43>(d, q, k, e, residual, st, &done)
+                 : launch_gemm_rows<128, 44>(d, q, k, e, residual, st, &done);
+  if (rc || done) return rc;
   if (s_out)
     return residual ? launch_gemm_epilogue<true, true, 36>(d, q, k, e, residual, st)
                     : launch_gemm_epilogue<true, false, 37>(d, q, k, e, nullptr, st);

@@ -6,7 +6,8 @@
 // rows are the 128 rows of the MMA and the tokens its N = 32, 64 or 128 columns
 // (Y^T = W X^T; an activation of 17 rows fills 17 of 32 columns instead of 17
 // of 256 rows), and K is split over the S = 1, 2, 4 or 8 blocks of a cluster, so
-// that N / 128 x S blocks cover the SMs.  Each block sums its K range in TMEM;
+// that N / 128 x S blocks cover the SMs (more rows than 128, where N is small,
+// are further tiles).  Each block sums its K range in TMEM;
 // the ranges' sums meet in shared memory across the cluster, each block
 // finishing NTOK / S of the tokens: the others' shares come by bulk copies (a
 // store of each lane into the other block took 0.2 us a token), it adds the S
@@ -54,8 +55,8 @@ template <int NTOK>
 __global__ void __launch_bounds__(kRowsThreads, 1)
     fp8_gemm_rows_kernel(const __grid_constant__ CUtensorMap tm_w,
                          const __grid_constant__ CUtensorMap tm_x, const EpilogueArgs E,
-                         const uint16_t *residual, void *out, int M, int N, int K,
-                         int kb_per_block, uint64_t timeout_ns) {
+                         const uint16_t *residual, void *out, int all_rows, int N, int K,
+                         int row_tiles, int kb_per_block, uint64_t timeout_ns) {
   using C = RowsCfg<NTOK>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -73,7 +74,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
   uint32_t S;  // blocks of the cluster
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
   const uint32_t rank = cluster_ctarank();
-  const int n0 = static_cast<int>(blockIdx.x / S) * 128;
+  const int tile = static_cast<int>(blockIdx.x / S);
+  const int n0 = tile / row_tiles * 128, row0 = tile % row_tiles * NTOK;
+  const int M = min(NTOK, all_rows - row0);  // tokens of this tile
   const int num_kb = (K + kGemmBK - 1) / kGemmBK;
   const int kb0 = static_cast<int>(rank) * kb_per_block;
   const int kb1 = min(kb0 + kb_per_block, num_kb);
@@ -119,7 +122,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         }
         mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
         tma_load_2d(sW + s * C::W_BYTES, &tm_w, &full[s], kb * kGemmBK, n0);
-        tma_load_2d(sX + s * C::X_BYTES, &tm_x, &full[s], kb * kGemmBK, 0);
+        tma_load_2d(sX + s * C::X_BYTES, &tm_x, &full[s], kb * kGemmBK, row0);
       }
       if (!ok) {  // loads in flight land before the block may end
         int zero = 0;
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
       for (int y = 0; y < RUN; ++y)
         res[y] = residual && x0 + y < count
                      ? __uint_as_float(static_cast<uint32_t>(
-                                           residual[static_cast<int64_t>(m0 + x0 + y) * N + n])
+                                           residual[static_cast<int64_t>(row0 + m0 + x0 + y) * N + n])
                                        << 16)
                      : 0.0f;
     };
@@ -239,7 +242,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         }
         v[y] += res[y];
         if (x0 + y < count) {
-          const int64_t at = static_cast<int64_t>(m0 + x0 + y) * N + n;
+          const int64_t at = static_cast<int64_t>(row0 + m0 + x0 + y) * N + n;
           if (E.s_out)
             static_cast<uint8_t *>(out)[at] =
                 static_cast<uint8_t>(cvt_e4m3x2(v[y] * inv_out, 0.0f));

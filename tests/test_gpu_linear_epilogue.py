@@ -83,8 +83,8 @@ def test_against_the_formula(M, N, K, bias, act, residual, fp8):
     check(y, v, a, K, s_out)
 
 
-@pytest.mark.parametrize("M", [31, 32, 33, 63, 64, 65, 100, 127, 128, 129])
-@pytest.mark.parametrize("N,K", [(528, 2048), (96, 4112), (6000, 384)])
+@pytest.mark.parametrize("M", [31, 32, 33, 63, 64, 65, 100, 127, 128, 129, 255, 256, 257, 700])
+@pytest.mark.parametrize("N,K", [(528, 2048), (96, 4112), (6000, 384), (264, 1424), (272, 1536)])
 def test_row_counts_where_the_kernel_changes(M, N, K):
     """The kernels' borders in rows, each with K split over a cluster in
     several ways (its last range short), and the same bits again."""
