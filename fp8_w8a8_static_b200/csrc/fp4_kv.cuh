@@ -26,11 +26,20 @@ namespace fp8ws {
 
 constexpr int kStripTokens = 16;
 constexpr int kKvThreads = 256;
+// Blocks an SM of the append and gather kernels: 48 registers a thread.  Their
+// rounds are chains of slot, values, codes and store, so it is the warps that
+// hide them (8191 x 8 x 128, both: 24.7 us with 54 registers and four blocks, 22.8
+// with five, 23.5 with six or eight).
+constexpr int kKvBlocks = 5;
 
 __host__ __device__ constexpr int strip_bytes(int D) { return 18 * D; }
 __host__ __device__ constexpr int strip_v(int D) { return 8 * D; }
 __host__ __device__ constexpr int strip_ks(int D) { return 16 * D; }
 __host__ __device__ constexpr int strip_vs(int D) { return 17 * D; }
+
+__device__ __forceinline__ void halves(uint64_t v, float &lo, float &hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
 
 // Eight fp32 values -> eight E2M1 codes, value 0 in the lowest nibble
 // (nearest, ties to even, saturating at +-6).
@@ -77,6 +86,28 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// The (token, head) of a thread's units, which lie `stride` apart: one division
+// for all of them.
+struct UnitWalk {
+  int64_t token, d_token;
+  int head, d_head, heads;
+  __device__ UnitWalk(int64_t u, int64_t stride, int64_t units, int n) : heads(n) {
+    const bool small = units <= INT32_MAX && stride <= INT32_MAX;
+    token = small ? static_cast<uint32_t>(u) / static_cast<uint32_t>(n) : u / n;
+    d_token = small ? static_cast<uint32_t>(stride) / static_cast<uint32_t>(n) : stride / n;
+    head = static_cast<int>(u - token * n);
+    d_head = static_cast<int>(stride - d_token * n);
+  }
+  __device__ void next() {
+    token += d_token;
+    head += d_head;
+    if (head >= heads) {
+      head -= heads;
+      ++token;
+    }
+  }
+};
+
 struct KvCache {
   uint8_t *data;
   int64_t pages;
@@ -97,27 +128,32 @@ __device__ __forceinline__ int64_t strip_offset(const KvCache &c, int64_t slot, 
 // A lane owns the 16 values of a scale, so nothing is exchanged but the NaN
 // ballot: D/16 lanes for a token's K of one head, D/16 for its V.  Bound by the
 // values' bytes (2 read, 0.56 written).  An IEEE division per value would cost
-// more than the stream (append and gather of 8191 x 8 x 128: 35 us with it, 24.5
+// more than the stream (append and gather of 8191 x 8 x 128: 35 us with it, 22.8
 // without), so a code is first bracketed: with r = fl32(1 / by), x fl32(r (1 -
 // 2^-20)) and x fl32(r (1 + 2^-20)) lie on either side of fl32(x / by) (each of
 // their two roundings, and the quotient's, is 2^-24); where both have one code
 // it is the quotient's, and only lanes with a code that differs divide.  Two or
-// four units of a lane in flight were not faster: the resident blocks have
-// enough loads out.
+// four units of a lane in flight were not faster: they cost resident blocks.
 
-// Codes of x[8] / by, the IEEE quotient's.  r is 1 / by, 0 to divide at once.
-__device__ __forceinline__ uint32_t quotient_codes(const float (&x)[8], float by, float r) {
-  const float lo = __fmul_rn(r, 1.0f - 0x1p-20f), hi = __fmul_rn(r, 1.0f + 0x1p-20f);
+// Codes of the 8 BF16 values of w over `by`, the IEEE quotient's.  r is 1 / by, 0
+// to divide at once.
+__device__ __forceinline__ uint32_t quotient_codes(const uint32_t *w, float by, float r) {
+  const float l = __fmul_rn(r, 1.0f - 0x1p-20f), h = __fmul_rn(r, 1.0f + 0x1p-20f);
+  const uint64_t lo = f32x2(l, l), hi = f32x2(h, h);
   float p[8], q[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    p[i] = __fmul_rn(x[i], lo);
-    q[i] = __fmul_rn(x[i], hi);
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t x = f32x2(bf16_lo(w[i]), bf16_hi(w[i]));
+    halves(mul_f32x2(x, lo), p[2 * i], p[2 * i + 1]);
+    halves(mul_f32x2(x, hi), q[2 * i], q[2 * i + 1]);
   }
   const uint32_t a = cvt_e2m1x8(p), b = cvt_e2m1x8(q);
   if (a == b && r != 0.0f) return a;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) p[i] = __fdiv_rn(x[i], by);
+  for (int i = 0; i < 4; ++i) {
+    p[2 * i] = __fdiv_rn(bf16_lo(w[i]), by);
+    p[2 * i + 1] = __fdiv_rn(bf16_hi(w[i]), by);
+  }
   return cvt_e2m1x8(p);
 }
 
@@ -146,25 +182,11 @@ __device__ __forceinline__ uint2 quantize16(const uint4 (&w)[2], float s, float 
   const float by = __fmul_rn(e4m3_to_float(scale), s);
   if (!(by > 0.0f)) return make_uint2(0, 0);
   const float r = by > 0x1p-120f && by < 0x1p120f ? __frcp_rn(by) : 0.0f;
-  uint2 codes;
-  float x[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16_lo(raw[i]);
-    x[2 * i + 1] = bf16_hi(raw[i]);
-  }
-  codes.x = quotient_codes(x, by, r);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16_lo(raw[4 + i]);
-    x[2 * i + 1] = bf16_hi(raw[4 + i]);
-  }
-  codes.y = quotient_codes(x, by, r);
-  return codes;
+  return make_uint2(quotient_codes(raw, by, r), quotient_codes(raw + 4, by, r));
 }
 
 template <int D>
-__global__ void __launch_bounds__(kKvThreads)
+__global__ void __launch_bounds__(kKvThreads, kKvBlocks)
     fp4_kv_append_kernel(const uint16_t *__restrict__ k, const uint16_t *__restrict__ v,
                          const int64_t *__restrict__ slots, int64_t units, const float *s_k,
                          const float *s_v, const KvCache c) {
@@ -181,19 +203,18 @@ __global__ void __launch_bounds__(kKvThreads)
   const int64_t stride = static_cast<int64_t>(gridDim.x) * UNITS;
   const uint32_t mine = ((1u << LANES) - 1u) << (threadIdx.x % 32 / LANES * LANES);
   const uint16_t *from = is_v ? v : k;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * UNITS;
+  UnitWalk at(first + threadIdx.x / LANES, stride, units + UNITS, c.heads);
   // every lane of a warp runs the same number of rounds (the ballot below)
-  for (int64_t u0 = static_cast<int64_t>(blockIdx.x) * UNITS; u0 < units; u0 += stride) {
+  for (int64_t u0 = first; u0 < units; u0 += stride, at.next()) {
     const int64_t u = u0 + threadIdx.x / LANES;
     uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
     int64_t slot = -1;
-    int head = 0;
     if (u < units) {
       const uint4 *src = reinterpret_cast<const uint4 *>(from + u * D) + 2 * part;
       w[0] = ld_stream(src);
       w[1] = ld_stream(src + 1);
-      const int64_t token = units <= INT32_MAX ? static_cast<uint32_t>(u) / c.heads : u / c.heads;
-      head = static_cast<int>(u - token * c.heads);
-      slot = __ldg(slots + token);
+      slot = __ldg(slots + at.token);
     }
     uint32_t scale;
     bool nan;
@@ -201,7 +222,7 @@ __global__ void __launch_bounds__(kKvThreads)
     const uint32_t nans = __ballot_sync(0xFFFFFFFFu, nan);
     if (!is_v && (nans & mine)) scale = 0x7Fu;
     if (slot < 0 || slot >= n_slots) continue;
-    uint8_t *strip = c.data + strip_offset<D>(c, slot, head);
+    uint8_t *strip = c.data + strip_offset<D>(c, slot, at.head);
     const int row = static_cast<int>(slot & (kStripTokens - 1));
     *reinterpret_cast<uint2 *>(strip + (is_v ? strip_v(D) : 0) + row * (D / 2) + part * 8) = codes;
     strip[(is_v ? strip_vs(D) : strip_ks(D)) + row * (D / 16) + part] = static_cast<uint8_t>(scale);
@@ -210,7 +231,7 @@ __global__ void __launch_bounds__(kKvThreads)
 
 // ------------------------------------------------------------------ gather
 template <int D>
-__global__ void __launch_bounds__(kKvThreads)
+__global__ void __launch_bounds__(kKvThreads, kKvBlocks)
     fp4_kv_gather_kernel(const int64_t *__restrict__ slots, int64_t units, const float *s_k,
                          const float *s_v, const KvCache c, uint16_t *__restrict__ k,
                          uint16_t *__restrict__ v) {
@@ -225,15 +246,14 @@ __global__ void __launch_bounds__(kKvThreads)
   const int64_t n_slots = c.pages << c.page_shift;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * UNITS;
   uint16_t *to = is_v ? v : k;
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * UNITS + threadIdx.x / LANES; u < units;
-       u += stride) {
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * UNITS + threadIdx.x / LANES;
+  UnitWalk at(first, stride, units + UNITS, c.heads);
+  for (int64_t u = first; u < units; u += stride, at.next()) {
     uint2 codes = make_uint2(0, 0);
     uint32_t scale = 0;  // zeros for a slot outside the cache
-    const int64_t token = units <= INT32_MAX ? static_cast<uint32_t>(u) / c.heads : u / c.heads;
-    const int head = static_cast<int>(u - token * c.heads);
-    const int64_t slot = __ldg(slots + token);
+    const int64_t slot = __ldg(slots + at.token);
     if (slot >= 0 && slot < n_slots) {
-      const uint8_t *strip = c.data + strip_offset<D>(c, slot, head);
+      const uint8_t *strip = c.data + strip_offset<D>(c, slot, at.head);
       const int row = static_cast<int>(slot & (kStripTokens - 1));
       codes = *reinterpret_cast<const uint2 *>(strip + (is_v ? strip_v(D) : 0) + row * (D / 2) +
                                                part * 8);
