@@ -684,6 +684,7 @@ FP8WS_API int fp4_kv_gather(const uint8_t *cache, int64_t num_pages, int page_si
  * s_out NULL: out [total_q][q_heads][head_dim] BF16.  Else out holds FP8 codes
  * E4M3_satRNE(o / s_out[0]) (to within one step, as silu_mul_2in_fp8), o_proj's
  * input at its calibrated scale.  lse: device [total_q][q_heads] fp32, or NULL.
+ * out and lse overlap no input.
  * workspace: device, fp4_kv_attention_workspace() bytes, 256-byte aligned,
  * overwritten; calls that may overlap on the GPU need one each.
  * The result does not depend on timing (no atomics): the same call gives the

@@ -116,8 +116,9 @@ def test_plain_is_fp8_linear_static(M):
 
 
 @pytest.mark.parametrize("M", [5, 33, 64, 100, 600])
-def test_residual_in_place(M):
-    xq, wq, b, r = make(M, 528, 256, M)
+@pytest.mark.parametrize("K", [256, 1552])
+def test_residual_in_place(M, K):
+    xq, wq, b, r = make(M, 528, K, M)
     want = fw.fp8_linear_epilogue(xq, wq, one(S_IN), one(S_W), b, "none", r)
     got = r.clone()
     fw.fp8_linear_epilogue(xq, wq, one(S_IN), one(S_W), b, "none", got, out=got)
