@@ -603,8 +603,9 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
       ok = wait(&pv_done[tile][(chunks - 1) & 1], (chunks - 1) >> 1);
       tc_fence_after();
     }
-    if (used && ok && a.splits > 1) {  // sums as they are
+    if (used && ok && a.splits > 1) {  // sums as they are, [D / 4][256 rows][4]
       const int64_t slot = static_cast<int64_t>(blockIdx.x) * kKvTileRows + r;
+      float *to = a.part + static_cast<int64_t>(blockIdx.x) * kKvTileRows * D + 4 * r;
 #pragma unroll 1
       for (int col = 0; chunks > 0 && col < D; col += 32) {
         uint32_t o[32];
@@ -613,7 +614,7 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
         if (!live) continue;
 #pragma unroll
         for (int x = 0; x < 32; x += 4)
-          *reinterpret_cast<uint4 *>(a.part + slot * D + col + x) =
+          *reinterpret_cast<uint4 *>(to + (col + x) * kKvTileRows) =
               make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
       }
       float *ml = a.part + static_cast<int64_t>(kKvTileSlots) * kKvTileRows * D;
@@ -676,18 +677,20 @@ __global__ void __launch_bounds__(kKvTileMergeThreads)
   pdl_wait();
   const int item = static_cast<int>(blockIdx.x) / BLOCKS;
   const int4 w = a.meta[item];
-  const int r = static_cast<int>(blockIdx.x) % BLOCKS * ROWS + static_cast<int>(threadIdx.x) / LANES;
+  // neighbouring threads: the block's rows, then the next four values
+  const int r = static_cast<int>(blockIdx.x) % BLOCKS * ROWS + static_cast<int>(threadIdx.x) % ROWS;
   if (w.x < 0 || r >= w.w) return;
-  const int lane = threadIdx.x % LANES;
+  const int lane = threadIdx.x / ROWS;
   const float2 *ml = reinterpret_cast<const float2 *>(
       a.part + static_cast<int64_t>(kKvTileSlots) * kKvTileRows * D);
   float top = -INFINITY, sum = 0.0f;
   float4 val = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
   for (int s = 0; s < a.splits; ++s) {
-    const int64_t slot = static_cast<int64_t>(item * a.splits + s) * kKvTileRows + r;
-    const float2 p = ml[slot];
-    const float4 v = *reinterpret_cast<const float4 *>(a.part + slot * D + 4 * lane);
+    const int64_t slot = static_cast<int64_t>(item * a.splits + s) * kKvTileRows;
+    const float2 p = ml[slot + r];
+    const float4 v = *reinterpret_cast<const float4 *>(a.part + slot * D +
+                                                       4 * (lane * kKvTileRows + r));
     // nothing seen there, and nothing written where it had no chunk; but a NaN sum counts
     if (p.x == -INFINITY && p.y == 0.0f) continue;
     const float now = fmaxf(top, p.x);
