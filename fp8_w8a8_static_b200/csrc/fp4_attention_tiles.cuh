@@ -23,15 +23,15 @@
 // Bound, for 256 rows and 64 tokens: 2 x (390 + 260) cycles of the tensor pipe
 // (D = 128; the first product, N = 64, is held by the reads of Q) beside 1024 of
 // the special function unit (one exponential a score, 16 a cycle).  Measured
-// (24 query heads on 8 K/V heads of 128, 2 x 2048 rows over 3000 to 8192 tokens):
-// 278 us, about 2200 cycles a chunk, the rest being what the warps wait for one
+// (24 query heads on 8 K/V heads of 128, two requests, 2048 rows behind 8192 tokens
+// and 1266 behind 4226): 274 us, about 2200 cycles a chunk, the rest being what the warps wait for one
 // another; 45 us for 4096 rows over 1024 tokens, 64-wide heads.
 // On the way, for the first of them: 350 us with chunks of 128 tokens and one score
 // buffer, 315 with half of a chunk's weights handed over at a time, 320 as now but
 // with each MMA issued from one thread's own registers, 283 with the issue
-// warp-uniform, 278 with packed fp32 pairs in the softmax.  Ranges of tokens cut
-// evenly over persistent blocks were slower (300 us): nearly every range then
-// leaves partial sums.
+// warp-uniform, 278 with packed fp32 pairs in the softmax, 274 with 16-byte stores
+// of FP8 output.  Ranges of tokens cut evenly over persistent blocks were slower
+// (300 us): nearly every range then leaves partial sums.
 #pragma once
 
 #include "common.cuh"
@@ -629,26 +629,33 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
           tmem_ld_32x32b_x32(t_o + col, o);
           tmem_ld_wait();
         }
+        float v[32];
 #pragma unroll
-        for (int x = 0; x < 32; x += 8) {
-          float v[8];
+        for (int x = 0; x < 32; ++x)
+          v[x] = chunks > 0 && l != 0.0f ? __uint_as_float(o[x]) * by : 0.0f;
+        if (!live) continue;
+        if (a.s_out) {
+          uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + at * D + col);
 #pragma unroll
-          for (int y = 0; y < 8; ++y)
-            v[y] = chunks > 0 && l != 0.0f ? __uint_as_float(o[x + y]) * by : 0.0f;
-          if (!live) continue;
-          if (a.s_out) {
-            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + at * D + col + x) =
-                make_uint2(pack4(cvt_e4m3x2(v[0], v[1]), cvt_e4m3x2(v[2], v[3])),
-                           pack4(cvt_e4m3x2(v[4], v[5]), cvt_e4m3x2(v[6], v[7])));
-          } else {
+          for (int x = 0; x < 32; x += 16) {
+            uint32_t h[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              h[y] = pack4(cvt_e4m3x2(v[x + 4 * y], v[x + 4 * y + 1]),
+                           cvt_e4m3x2(v[x + 4 * y + 2], v[x + 4 * y + 3]));
+            to[x / 16] = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        } else {
+          uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at * D + col);
+#pragma unroll
+          for (int x = 0; x < 32; x += 8) {
             uint32_t h[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              const __nv_bfloat162 z = __floats2bfloat162_rn(v[2 * y], v[2 * y + 1]);
+              const __nv_bfloat162 z = __floats2bfloat162_rn(v[x + 2 * y], v[x + 2 * y + 1]);
               h[y] = *reinterpret_cast<const uint32_t *>(&z);
             }
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at * D + col + x) =
-                make_uint4(h[0], h[1], h[2], h[3]);
+            to[x / 8] = make_uint4(h[0], h[1], h[2], h[3]);
           }
         }
       }
