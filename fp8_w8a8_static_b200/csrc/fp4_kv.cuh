@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(THREADS) fp4_kv_tables_kernel(const TableArgs 
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int rank = blockIdx.x, ranks = gridDim.x;
   const int64_t used = max(0, *a.used);
-  int64_t rows = 0, pages = 0;  // of the requests before this round
+  int64_t rows = 0, pages = 0;  // of the requests before this turn
   for (int b0 = 0; b0 < a.batch; b0 += THREADS) {
     const int b = b0 + static_cast<int>(threadIdx.x);
     int64_t old = 0, add = 0;
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(THREADS) fp4_kv_tables_kernel(const TableArgs 
       warp_rows[warp] = r;
       warp_pages[warp] = p;
     }
-    // also: every block has read this round's lengths, which kv_lens may replace
+    // also: every block has read this turn's lengths, which kv_lens may replace
     cluster_sync();
     int64_t all_rows = 0, all_pages = 0;
 #pragma unroll 8
