@@ -273,6 +273,27 @@ def _device_of(t: torch.Tensor):
     return torch.cuda.device(t.device)
 
 
+def _allocating_on(stream, device):
+    """Makes a call's stream the current one for what the call allocates.  The
+    caching allocator hands out memory of the current stream that earlier work
+    of that stream may still use, which only that stream is ordered behind."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)  # 1: the legacy default stream's other handle
+        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=device)
+    return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A result of a call on `stream`.  It is the caller's, who reads it on the
+    current stream: freed, it is not handed out again before that work is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _allocating_on(stream, device):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 # ---------------------------------------------------------------- hot path
 
 
@@ -281,7 +302,7 @@ def fp8_quant_static(x: torch.Tensor, s_in: torch.Tensor, out: Optional[torch.Te
     """Xq = E4M3_satRNE(x / s_in), any shape, BF16 in, FP8 out."""
     lib = load()
     if out is None:
-        out = torch.empty(x.shape, dtype=FP8, device=x.device)
+        out = _empty(x.shape, FP8, x.device, stream)
     if out.numel() != x.numel():
         raise ValueError("out size differs from x")
     with _device_of(x):
@@ -299,7 +320,7 @@ def fp8_linear_static(xq: torch.Tensor, wq: torch.Tensor, s_in: torch.Tensor, s_
     M, K = xq.shape
     N = wq.shape[0]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+        out = _empty((M, N), torch.bfloat16, xq.device, stream)
     if tuple(out.shape) != (M, N):
         raise ValueError("out must be [M, N]")
     with _device_of(xq):
@@ -316,9 +337,9 @@ def fp8_linear_static_ws(xq, wq, s_in, s_w, workspace=None, out=None, stream=Non
     N = wq.shape[0]
     need = lib.fp8_linear_static_ws_bytes()
     if workspace is None:
-        workspace = _workspace(need, xq.device)
+        workspace = _workspace(need, xq.device, stream)
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+        out = _empty((M, N), torch.bfloat16, xq.device, stream)
     with _device_of(xq):
         _check(lib.fp8_linear_static_ws(_fp8(xq, "xq"), _fp8(wq, "wq"), M, N, K, _f32(s_in, "s_in"),
                                         _f32(s_w, "s_w"), _bf16(out, "out"),
@@ -335,7 +356,7 @@ def silu_mul_2in_fp8(g: torch.Tensor, u: torch.Tensor, s_down: torch.Tensor,
     if g.shape != u.shape:
         raise ValueError("G and U shapes differ")
     if out is None:
-        out = torch.empty(g.shape, dtype=FP8, device=g.device)
+        out = _empty(g.shape, FP8, g.device, stream)
     if out.numel() != g.numel():
         raise ValueError("out size differs from G")
     with _device_of(g):
@@ -349,9 +370,12 @@ def gated_mlp_static_fp8_workspace(M: int, d: int, I: int) -> int:
     return load().gated_mlp_static_fp8_workspace(M, d, I)
 
 
-def _workspace(nbytes: int, device) -> torch.Tensor:
+def _workspace(nbytes: int, device, stream) -> torch.Tensor:
     # torch's caching allocator hands out 512-byte aligned blocks
-    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    if stream is None:
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    with _allocating_on(stream, device):
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
 def gated_mlp_static_fp8(x, s_in, wg, s_wg, wu, s_wu, s_down, wd, s_wd, workspace=None, out=None,
@@ -367,11 +391,11 @@ def gated_mlp_static_fp8(x, s_in, wg, s_wg, wu, s_wu, s_down, wd, s_wd, workspac
         raise ValueError("weight shapes must be Wg, Wu [I,d] and Wd [d,I]")
     need = lib.gated_mlp_static_fp8_workspace(M, d, I)
     if workspace is None:
-        workspace = _workspace(need, x.device)
+        workspace = _workspace(need, x.device, stream)
     if workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace needs {need} bytes")
     if out is None:
-        out = torch.empty((M, d), dtype=torch.bfloat16, device=x.device)
+        out = _empty((M, d), torch.bfloat16, x.device, stream)
     with _device_of(x):
         _check(lib.gated_mlp_static_fp8(
             _bf16(x, "x"), M, d, I, _f32(s_in, "s_in"), _fp8(wg, "wg"), _f32(s_wg, "s_wg"),
@@ -404,7 +428,7 @@ def swiglu_2in_fp8(g: torch.Tensor, u: torch.Tensor, s_down: torch.Tensor, act=N
     if g.shape != u.shape:
         raise ValueError("G and U shapes differ")
     if out is None:
-        out = torch.empty(g.shape, dtype=FP8, device=g.device)
+        out = _empty(g.shape, FP8, g.device, stream)
     with _device_of(g):
         _check(lib.swiglu_2in_fp8(_bf16(g, "g"), _bf16(u, "u"), g.numel(), _f32(s_down, "s_down"),
                                   _act(act), _fp8(out, "out"), _stream(stream)), "swiglu_2in_fp8")
@@ -421,7 +445,7 @@ def fp8_gate_up_swiglu_static(xq, wg, wu, s_in, s_wg, s_wu, s_down, act=None, ou
     if tuple(wg.shape) != (I, K) or tuple(wu.shape) != (I, K):
         raise ValueError("Wg and Wu must both be [I, K]")
     if out is None:
-        out = torch.empty((M, I), dtype=FP8, device=xq.device)
+        out = _empty((M, I), FP8, xq.device, stream)
     with _device_of(xq):
         _check(lib.fp8_gate_up_swiglu_static(
             _fp8(xq, "xq"), _fp8(wg, "wg"), _fp8(wu, "wu"), M, I, K, _f32(s_in, "s_in"),
@@ -448,11 +472,11 @@ def gated_mlp_static_fp8_fused(x, s_in, wg, s_wg, wu, s_wu, s_down, wd, s_wd, wo
         raise ValueError("weight shapes must be Wg, Wu [I,d] and Wd [d,I]")
     need = lib.gated_mlp_static_fp8_fused_workspace(M, d, I)
     if workspace is None:
-        workspace = _workspace(need, x.device)
+        workspace = _workspace(need, x.device, stream)
     if workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace needs {need} bytes")
     if out is None:
-        out = torch.empty((M, d), dtype=torch.bfloat16, device=x.device)
+        out = _empty((M, d), torch.bfloat16, x.device, stream)
     with _device_of(x):
         _check(lib.gated_mlp_static_fp8_fused(
             _bf16(x, "x"), M, d, I, _f32(s_in, "s_in"), _fp8(wg, "wg"), _f32(s_wg, "s_wg"),
@@ -484,7 +508,7 @@ def fp8_quant_static_group(xs, scales, outs=None, stream=None):
     if len(xs) != len(scales):
         raise ValueError("one scale per activation")
     if outs is None:
-        outs = [torch.empty(x.shape, dtype=FP8, device=x.device) for x in xs]
+        outs = [_empty(x.shape, FP8, x.device, stream) for x in xs]
     for x, o in zip(xs, outs):
         if o.numel() != x.numel():
             raise ValueError("out size differs from x")
@@ -504,7 +528,7 @@ def fp8_linear_static_group(problems, outs=None, split_k=False, workspace=None, 
     lib = load()
     N, K = problems[0][1].shape
     if outs is None:
-        outs = [torch.empty((xq.shape[0], N), dtype=torch.bfloat16, device=xq.device)
+        outs = [_empty((xq.shape[0], N), torch.bfloat16, xq.device, stream)
                 for xq, *_ in problems]
     items = []
     for (xq, wq, s_in, s_w), y in zip(problems, outs):
@@ -518,7 +542,7 @@ def fp8_linear_static_group(problems, outs=None, split_k=False, workspace=None, 
     ws_ptr, ws_bytes = None, 0
     if split_k:
         if workspace is None:
-            workspace = _workspace(lib.fp8_linear_static_ws_bytes(), problems[0][0].device)
+            workspace = _workspace(lib.fp8_linear_static_ws_bytes(), problems[0][0].device, stream)
         ws_ptr = _dev_ptr(workspace, "workspace", (torch.uint8,))
         ws_bytes = workspace.numel() * workspace.element_size()
     with _device_of(problems[0][0]):
@@ -533,7 +557,7 @@ def fp8_gate_up_swiglu_static_group(problems, act=None, outs=None, stream=None):
     lib = load()
     I, K = problems[0][1].shape
     if outs is None:
-        outs = [torch.empty((p[0].shape[0], I), dtype=FP8, device=p[0].device) for p in problems]
+        outs = [_empty((p[0].shape[0], I), FP8, p[0].device, stream) for p in problems]
     items = []
     for (xq, wg, wu, s_in, s_wg, s_wu, s_down), h in zip(problems, outs):
         if tuple(wg.shape) != (I, K) or tuple(wu.shape) != (I, K) or xq.shape[1] != K:
@@ -579,9 +603,9 @@ def gated_mlp_static_fp8_group(towers, act=None, workspace=None, outs=None, stre
             raise ValueError("weight shapes must be Wg, Wu [I,d] and Wd [d,I], shared d and I")
     need = gated_mlp_static_fp8_group_workspace(Ms, d, I)
     if workspace is None:
-        workspace = _workspace(need, towers[0]["x"].device)
+        workspace = _workspace(need, towers[0]["x"].device, stream)
     if outs is None:
-        outs = [torch.empty((M, d), dtype=torch.bfloat16, device=t["x"].device)
+        outs = [_empty((M, d), torch.bfloat16, t["x"].device, stream)
                 for M, t in zip(Ms, towers)]
     items = []
     for t, y in zip(towers, outs):
@@ -627,11 +651,11 @@ def qkv_shared_quant(x, s_in, wq, s_wq, wk, s_wk, wv, s_wv, workspace=None, out=
             raise ValueError(f"{n} must be [N, {d}]")
     need = lib.qkv_shared_quant_workspace(M, d)
     if workspace is None:
-        workspace = _workspace(need, x.device)
+        workspace = _workspace(need, x.device, stream)
     if workspace.numel() * workspace.element_size() < need:
         raise ValueError(f"workspace needs {need} bytes")
     if out is None:
-        out = tuple(torch.empty((M, n), dtype=torch.bfloat16, device=x.device) for n in (Nq, Nk, Nv))
+        out = tuple(_empty((M, n), torch.bfloat16, x.device, stream) for n in (Nq, Nk, Nv))
     q, k, v = out
     with _device_of(x):
         _check(lib.qkv_shared_quant(
@@ -652,11 +676,11 @@ def fp8_shared_quant_linears(x, s_in, projections, workspace=None, out=None, str
         if w.dim() != 2 or w.shape[1] != d:
             raise ValueError(f"projection {i} must be [N, {d}]")
     if out is None:
-        out = [torch.empty((M, w.shape[0]), dtype=torch.bfloat16, device=x.device)
+        out = [_empty((M, w.shape[0]), torch.bfloat16, x.device, stream)
                for w, _ in projections]
     need = lib.fp8_shared_quant_linears_workspace(M, d)
     if workspace is None:
-        workspace = _workspace(need, x.device)
+        workspace = _workspace(need, x.device, stream)
     W = (ctypes.c_void_p * n)(*[_fp8(w, f"W[{i}]") for i, (w, _) in enumerate(projections)])
     N = (ctypes.c_int64 * n)(*[w.shape[0] for w, _ in projections])
     S = (ctypes.c_void_p * n)(*[_f32(sw, f"s_w[{i}]") for i, (_, sw) in enumerate(projections)])
@@ -679,7 +703,7 @@ def fp8_linears_static(xq, s_in, projections, out=None, workspace=None, stream=N
         if w.dim() != 2 or w.shape[1] != K:
             raise ValueError(f"projection {i} must be [N, {K}]")
     if out is None:
-        out = [torch.empty((M, w.shape[0]), dtype=torch.bfloat16, device=xq.device)
+        out = [_empty((M, w.shape[0]), torch.bfloat16, xq.device, stream)
                for w, _ in projections]
     W = (ctypes.c_void_p * n)(*[_fp8(w, f"W[{i}]") for i, (w, _) in enumerate(projections)])
     N = (ctypes.c_int64 * n)(*[w.shape[0] for w, _ in projections])
@@ -703,13 +727,13 @@ def cross_attention_qkv_static_fp8(x, ctx, s_q, wq, s_wq, s_kv, wk, s_wk, wv, s_
     Mq, d = x.shape
     Mkv = ctx.shape[0]
     if out is None:
-        out = (torch.empty((Mq, wq.shape[0]), dtype=torch.bfloat16, device=x.device),
-               torch.empty((Mkv, wk.shape[0]), dtype=torch.bfloat16, device=x.device),
-               torch.empty((Mkv, wv.shape[0]), dtype=torch.bfloat16, device=x.device))
+        out = (_empty((Mq, wq.shape[0]), torch.bfloat16, x.device, stream),
+               _empty((Mkv, wk.shape[0]), torch.bfloat16, x.device, stream),
+               _empty((Mkv, wv.shape[0]), torch.bfloat16, x.device, stream))
     q, k, v = out
     need = lib.cross_attention_qkv_static_fp8_workspace(Mq, Mkv, d)
     if workspace is None:
-        workspace = _workspace(need, x.device)
+        workspace = _workspace(need, x.device, stream)
     with _device_of(x):
         _check(lib.cross_attention_qkv_static_fp8(
             _bf16(x, "x"), Mq, _bf16(ctx, "ctx"), Mkv, d, _f32(s_q, "s_q"), _fp8(wq, "wq"),
@@ -729,9 +753,9 @@ def fp8_quant_per_token(x: torch.Tensor, out=None, scales=None, stream=None):
     lib = load()
     rows, K = x.shape
     if out is None:
-        out = torch.empty((rows, K), dtype=FP8, device=x.device)
+        out = _empty((rows, K), FP8, x.device, stream)
     if scales is None:
-        scales = torch.empty(rows, dtype=torch.float32, device=x.device)
+        scales = _empty(rows, torch.float32, x.device, stream)
     with _device_of(x):
         _check(lib.fp8_quant_per_token(_bf16(x, "x"), rows, K, _dev_ptr(scales, "s", (torch.float32,)),
                                        _fp8(out, "out"), _stream(stream)), "fp8_quant_per_token")
@@ -747,7 +771,7 @@ def fp8_linear_scaled(xq, wq, s_x, s_w, out=None, stream=None) -> torch.Tensor:
     if s_x.numel() not in (1, M) or s_w.numel() not in (1, N):
         raise ValueError("s_x must hold 1 or M values, s_w 1 or N values")
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=xq.device)
+        out = _empty((M, N), torch.bfloat16, xq.device, stream)
     with _device_of(xq):
         _check(lib.fp8_linear_scaled(_fp8(xq, "xq"), _fp8(wq, "wq"), M, N, K, _f32(s_x, "s_x"),
                                      int(s_x.numel() == M and M > 1), _f32(s_w, "s_w"),
@@ -761,9 +785,9 @@ def silu_mul_2in_fp8_per_token(g, u, out=None, scales=None, stream=None):
     lib = load()
     rows, I = g.shape
     if out is None:
-        out = torch.empty((rows, I), dtype=FP8, device=g.device)
+        out = _empty((rows, I), FP8, g.device, stream)
     if scales is None:
-        scales = torch.empty(rows, dtype=torch.float32, device=g.device)
+        scales = _empty(rows, torch.float32, g.device, stream)
     with _device_of(g):
         _check(lib.silu_mul_2in_fp8_per_token(_bf16(g, "g"), _bf16(u, "u"), rows, I,
                                               _dev_ptr(scales, "s", (torch.float32,)),
@@ -780,9 +804,9 @@ def gated_mlp_per_token_fp8(x, wg, s_wg, wu, s_wu, wd, s_wd, workspace=None, out
     I = wg.shape[0]
     need = lib.gated_mlp_per_token_fp8_workspace(M, d, I)
     if workspace is None:
-        workspace = _workspace(need, x.device)
+        workspace = _workspace(need, x.device, stream)
     if out is None:
-        out = torch.empty((M, d), dtype=torch.bfloat16, device=x.device)
+        out = _empty((M, d), torch.bfloat16, x.device, stream)
     with _device_of(x):
         _check(lib.gated_mlp_per_token_fp8(
             _bf16(x, "x"), M, d, I, _fp8(wg, "wg"), _f32(s_wg, "s_wg"), _fp8(wu, "wu"),
@@ -843,15 +867,11 @@ def _call(dev, fn, name, *args):
         raise FP8WSError(status, name)
 
 
-def _scratch(nbytes, like, stream):
-    """A workspace for one call on the given stream: memory of another stream
-    than the current one is not handed out again before that stream is done."""
-    ws = like.new_empty(max(nbytes, 256), dtype=torch.uint8)
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=like.device)
-        ws.record_stream(stream)
-    return ws
+def _new(like, shape, dtype, stream):
+    """_empty on like's device."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    return _empty(shape, dtype, like.device, stream)
 
 
 # ---------------------------------------- Linear with a fused epilogue
@@ -883,7 +903,7 @@ def fp8_linear_epilogue(xq, wq, s_in, s_w, bias=None, act="none", residual=None,
     dev, st = _on(xq, stream)
     bf16 = torch.bfloat16
     if out is None:
-        out = xq.new_empty((M, N), dtype=bf16 if s_out is None else FP8)
+        out = _new(xq, (M, N), bf16 if s_out is None else FP8, stream)
     _call(dev, lib.fp8_linear_epilogue, "fp8_linear_epilogue", _codes(xq, "xq", dev),
           _codes(wq, "wq", dev), M, N, K, _scalar(s_in, "s_in", dev), _scalar(s_w, "s_w", dev),
           None if bias is None else _ptr(bias, "bias", dev, bf16), kind,
@@ -935,8 +955,8 @@ def fp4_kv_tables(lens, added, block_table, free_pages, used, page_size: int, n_
     dev, st = _on(lens, stream)
     i32, i64 = torch.int32, torch.int64
     if out is None:
-        cu_q, kv_lens, pool = lens.new_empty(B + 1), lens.new_empty(B), lens.new_empty(2)
-        slots = lens.new_empty(n_slots, dtype=i64)
+        cu_q, kv_lens, pool = (_new(lens, n, i32, stream) for n in (B + 1, B, 2))
+        slots = _new(lens, n_slots, i64, stream)
         out = (cu_q, kv_lens, slots, pool)
     else:
         cu_q, kv_lens, slots, pool = out
@@ -985,8 +1005,7 @@ def fp4_kv_gather(cache, slots, s_k, s_v, out=None, stream=None):
     dev, st = _on(cache, stream)
     bf16 = torch.bfloat16
     if out is None:
-        out = (cache.new_empty((T, heads, dim), dtype=bf16),
-               cache.new_empty((T, heads, dim), dtype=bf16))
+        out = tuple(_new(cache, (T, heads, dim), bf16, stream) for _ in range(2))
     k, v = out
     if k.numel() != T * heads * dim or v.numel() != T * heads * dim:
         raise ValueError(f"out must be two tensors [T, {heads}, {dim}]")
@@ -1031,11 +1050,11 @@ def fp4_kv_attention(q, cu_q, kv_lens, block_table, cache, s_k, s_v, max_q: int,
     dev, st = _on(q, stream)
     bf16, f32, i32, u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
     if workspace is None:
-        workspace = _scratch(_attention_workspace(), q, stream)
+        workspace = _workspace(_attention_workspace(), q.device, stream)
     if out is None:
-        out = q.new_empty(shape, dtype=bf16 if s_out is None else FP8)
+        out = _new(q, shape, bf16 if s_out is None else FP8, stream)
     if return_lse and lse is None:
-        lse = q.new_empty(shape[:2], dtype=f32)
+        lse = _new(q, shape[:2], f32, stream)
     _call(dev, lib.fp4_kv_attention, "fp4_kv_attention", _ptr(q, "q", dev, bf16), shape[0],
           shape[1], B, _ptr(cu_q, "cu_q", dev, i32), _ptr(kv_lens, "kv_lens", dev, i32), max_q,
           _ptr(block_table, "block_table", dev, i32), table[1], _ptr(cache, "cache", dev, u8),
@@ -1062,7 +1081,7 @@ def fp8_check_shared_input_scale(scales: Sequence[torch.Tensor], stream=None) ->
 def fp8_absmax_bf16(x, out=None, stream=None) -> torch.Tensor:
     lib = load()
     if out is None:
-        out = torch.empty(1, dtype=torch.float32, device=x.device)
+        out = _empty(1, torch.float32, x.device, stream)
     with _device_of(x):
         _check(lib.fp8_absmax_bf16(_bf16(x, "x"), x.numel(), _f32(out, "out"), _stream(stream)),
                "fp8_absmax_bf16")
@@ -1074,7 +1093,7 @@ def fp8_silu_mul_absmax(g, u, out=None, stream=None) -> torch.Tensor:
     if g.shape != u.shape:
         raise ValueError("G and U shapes differ")
     if out is None:
-        out = torch.empty(1, dtype=torch.float32, device=g.device)
+        out = _empty(1, torch.float32, g.device, stream)
     with _device_of(g):
         _check(lib.fp8_silu_mul_absmax(_bf16(g, "g"), _bf16(u, "u"), g.numel(), _f32(out, "out"),
                                        _stream(stream)), "fp8_silu_mul_absmax")
@@ -1085,7 +1104,7 @@ def fp8_observer_scale(amaxes: torch.Tensor, c: float = OBSERVER_CONSTANT, out=N
                        stream=None) -> torch.Tensor:
     lib = load()
     if out is None:
-        out = torch.empty(1, dtype=torch.float32, device=amaxes.device)
+        out = _empty(1, torch.float32, amaxes.device, stream)
     with _device_of(amaxes):
         _check(lib.fp8_observer_scale(_f32(amaxes, "amaxes"), amaxes.numel(), float(c),
                                       _f32(out, "out"), _stream(stream)), "fp8_observer_scale")
@@ -1096,9 +1115,9 @@ def fp8_rtn_quantize_weight(w: torch.Tensor, wq=None, s_w=None, stream=None):
     """(Wq, s_w): RTN per-tensor weight quantization with s_w = max|W| / 448."""
     lib = load()
     if wq is None:
-        wq = torch.empty(w.shape, dtype=FP8, device=w.device)
+        wq = _empty(w.shape, FP8, w.device, stream)
     if s_w is None:
-        s_w = torch.empty(1, dtype=torch.float32, device=w.device)
+        s_w = _empty(1, torch.float32, w.device, stream)
     with _device_of(w):
         _check(lib.fp8_rtn_quantize_weight(_bf16(w, "w"), w.numel(), _f32(s_w, "s_w"),
                                            _fp8(wq, "wq"), _stream(stream)),
