@@ -47,9 +47,16 @@ constexpr int kKvSlots = 3;      // ring slots of a warp, up to 2 strips each
 constexpr int kKvMaxBlocks = 444;  // ranges at most: 148 SMs x 3 blocks
 // Blocks of an SM: 16 query rows take the registers of two (168 spill).
 __host__ __device__ constexpr int kv_blocks_per_sm(int NT) { return NT == 1 ? 3 : 2; }
-// p = 2^(s - m) may exceed 1 by this many powers of two before the running
-// maximum m is moved: FP16 holds 2^15, the sums are fp32
-constexpr float kKvSlack = 10.0f;
+// A weight is 2^(s - m + kKvLift), m the running maximum in log2 units, and m is
+// moved when a weight would pass 2^kKvTop, FP16's last whole power (the sums are
+// fp32).  The lift is room below for the small weights of a long tail: FP16 rounds
+// to half of 2^-10 down to 2^-14 and to half of 2^-24 below, so a weight is off by
+// 2^-11 of itself down to 2^-23 of the largest one, and by 2^-34 of the largest one
+// below.  The rest is room above, for maxima that move seldom: lifts of 0, 5 and 9
+// take the same time (2048 rows behind 8192 tokens and 1266 behind 4226: 273 us),
+// 11 takes 277 and 13 takes 297.
+constexpr float kKvTop = 15.0f;
+constexpr float kKvLift = 9.0f;
 
 __device__ __forceinline__ uint32_t scaled(uint32_t h, __half2 s) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&h), s);
@@ -406,7 +413,7 @@ __global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
     all_see = min(all_see, __shfl_xor_sync(0xFFFFFFFFu, all_see, 2));
 
     float o[NT][TILES][4];
-    float neg_m[NT][2], l[NT][2];  // minus the running maximum (log2 units), the sums
+    float neg_m[NT][2], l[NT][2];  // kKvLift - m, the sums of the weights
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -496,27 +503,26 @@ __global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
 #pragma unroll
           for (int z = 1; z < NS; ++z) top[y] = fmaxf(top[y], fmaxf(e[z][y], e[z][y + 2]));
         }
-        if (__any_sync(0xFFFFFFFFu, fmaxf(top[0], top[1]) > kKvSlack)) {
+        if (__any_sync(0xFFFFFFFFu, fmaxf(top[0], top[1]) > kKvTop)) {
           // move the maxima (at first from -inf) to the largest scores
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const float old = neg_m[n][y];
+            top[y] = neg_m[n][y];
             neg_m[n][y] = 0.0f;  // the scores themselves
-            top[y] = -old;
           }
           exponents();
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const float old = -top[y];
-            float now = top[y];
+            const float old = top[y];
+            float now = kKvLift - old;
 #pragma unroll
             for (int z = 0; z < NS; ++z) now = fmaxf(now, fmaxf(e[z][y], e[z][y + 2]));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1)
               now = fmaxf(now, __shfl_xor_sync(0xFFFFFFFFu, now, d));
             // nothing seen yet: sums and maximum stay as they are
-            const float by = now == -INFINITY ? 1.0f : ex2_approx(-now - old);
-            neg_m[n][y] = now == -INFINITY ? INFINITY : -now;
+            neg_m[n][y] = now == -INFINITY ? INFINITY : kKvLift - now;
+            const float by = now == -INFINITY ? 1.0f : ex2_approx(neg_m[n][y] - old);
             l[n][y] *= by;
 #pragma unroll
             for (int x = 0; x < TILES; ++x) {
@@ -532,7 +538,7 @@ __global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
           for (int y = 0; y < 4; ++y) e[z][y] = ex2_approx(e[z][y]);
           l[n][0] += e[z][0] + e[z][2];
           l[n][1] += e[z][1] + e[z][3];
-          // P is rounded to FP16 (2^-11 of each weight) for the second product
+          // P is rounded to FP16 (see kKvLift) for the second product
           p[z][n][0] = transpose_8x8(pack_f16(e[z][0], e[z][1]));
           p[z][n][1] = transpose_8x8(pack_f16(e[z][2], e[z][3]));
         }

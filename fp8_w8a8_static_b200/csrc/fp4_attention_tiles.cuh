@@ -17,7 +17,7 @@
 //                 registers from the search for the maximum to the weights.
 // Each row tile has two score buffers: while the softmax is on one chunk, the
 // next one's scores are computed.  A row's maximum is moved, and its sums in TMEM
-// scaled, only when a score exceeds it by 2^10 (FP16 weights have that room).
+// scaled, only when a weight would pass 2^kKvTop, what FP16 holds (kKvLift).
 // Where the row blocks do not fill the GPU, `splits` blocks share one's tokens
 // and leave partial sums, which fp4_kv_tiles_merge_kernel adds in order.
 // Bound, for 256 rows and 64 tokens: 2 x (390 + 260) cycles of the tensor pipe
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
     const bool used = tile < row_tiles;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t t_o = tmem + lanes + C::O_COL + tile * 128;
-    float neg_m = INFINITY, l = 0.0f;  // minus the maximum in log2 units, the sum
+    float neg_m = INFINITY, l = 0.0f;  // kKvLift - m, the sum of the weights
     bool ok = true;
     for (int i = 0; used && i < chunks; ++i) {
       ok = wait(&s_full[tile][i & 1], i >> 1);
@@ -554,11 +554,11 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
       }
       const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
       const float now = top == -INFINITY ? -INFINITY : top * c;
-      if (__any_sync(0xFFFFFFFFu, now + neg_m > kKvSlack)) {
+      if (__any_sync(0xFFFFFFFFu, now + neg_m > kKvTop)) {
         // move the maxima (at first from -inf); O must not be in use
-        const float next = fmaxf(-neg_m, now);
-        const float by = next == -INFINITY ? 1.0f : ex2_approx(-neg_m - next);
-        neg_m = next == -INFINITY ? INFINITY : -next;
+        const float next = fminf(neg_m, kKvLift - now);
+        const float by = next == INFINITY ? 1.0f : ex2_approx(next - neg_m);
+        neg_m = next;
         l *= by;
         if (i > 0) {
           ok = wait(&pv_done[tile][(i - 1) & 1], (i - 1) >> 1);
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kKvTileThreads, 1)
       const float shift = neg_m == INFINITY ? 0.0f : neg_m;
       const uint64_t c2 = pair(c, c), shift2 = pair(shift, shift);
       uint64_t sums = pair(0.0f, 0.0f);
-      // weights, rounded to FP16 (2^-11 of each) for the second product
+      // weights, rounded to FP16 (see kKvLift) for the second product
       auto weigh = [&](const uint32_t (&s)[32], uint32_t col) {
         uint32_t p[16];
 #pragma unroll

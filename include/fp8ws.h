@@ -674,7 +674,9 @@ FP8WS_API int fp4_kv_gather(const uint8_t *cache, int64_t num_pages, int page_si
  * Scores, maxima, sums and outputs are held in fp32; q enters the product as
  * FP16 times a power of two of its row (exact for elements above 2^-24 of the
  * row's largest), the cache's code * scale is exact in FP16, and the softmax
- * weights are rounded to FP16 (2^-11 of each weight) for the second product.
+ * weights are rounded to FP16 for the second product: by 2^-11 of a weight down to
+ * 2^-23 of the row's largest, by 2^-34 of the largest below (a token whose score is 24
+ * below the largest leaves the output, not lse).
  * q: device [total_q][q_heads][head_dim] BF16.  cu_q: device int32[batch + 1],
  * not decreasing.  kv_lens: device int32[batch].  max_q: at least the largest
  * number of rows of a request (it chooses the kernels; 0 launches nothing).

@@ -1,0 +1,93 @@
+"""How exact attention over the 4-bit cache is where many small weights make up
+the output: one dominant token whose V is 0 before a long uniform tail.
+
+Tolerances.  The weights are FP16 values of 2^(s - m + 9) (log2 units, m a running
+maximum no larger than the row's): half a step is 2^-11 of a weight from 2^-14 on,
+2^-25 below, which is 2^-34 of the largest weight (m at the maximum; less of it while
+m is behind).  With o the exact output, A = sum_j p_j |v_j| and Z = sum_j exp(s_j -
+max s), the output is off by at most
+  2^-8 |o|                  the output's rounding to BF16 (half a step)
+  (2^-11 + 2^-13) A         half a step of each weight, and the fp32 errors of
+                            scores (|s| <= 2^6 in log2 units here, each product
+                            exact: 2^-17 of the weight), exponentials and sums
+  n 2^-34 max|v| / Z        n weights below the normal range
+lse is fp32: 2^-19 of reach + |lse| + 1, reach = max_j sum |q k|."""
+
+import pytest
+import torch
+
+import fp8_w8a8_static_b200 as fw
+import _kv4
+from test_gpu_fp4_kv import DEV, S_K, S_V, ints, one
+
+pytestmark = pytest.mark.gpu
+PAGE = 64
+# rows of the request, query heads of the K/V head: the few-rows kernel with 8 and
+# with 16 rows, the many-rows kernel (whose blocks share the tokens)
+FORMS = [(1, 3), (6, 2), (300, 1), (1200, 1)]
+
+
+def stored(k, v):
+    """Cache and table with these tokens, and their exact values."""
+    n, heads, dim = k.shape
+    pages = -(-n // PAGE)
+    cache = fw.fp4_kv_cache(pages, heads, PAGE, dim, DEV)
+    fw.fp4_kv_append(k, v, torch.arange(n, device=DEV), cache, one(S_K), one(S_V))
+    kc, vc, ks, vs = _kv4.regions(cache)
+    s_k, s_v = (float(one(s)) for s in (S_K, S_V))
+    value = [_kv4.values(c, z, s).transpose(0, 1).reshape(heads, -1, dim)[:, :n]
+             for c, z, s in ((kc, ks, s_k), (vc, vs, s_v))]
+    return cache, ints([list(range(pages))]), value
+
+
+def formula(q, k, v, scale):
+    """(o, lse, A, Z, reach) in 64 bits of every row over every token."""
+    g = q.shape[1] // k.shape[0]
+    out = []
+    for r in range(q.shape[1]):
+        z = q[:, r].double() @ k[r // g].t() * scale
+        top = z.amax(1, keepdim=True)
+        w = torch.exp(z - top)
+        total = w.sum(1, keepdim=True)
+        p = w / total
+        out.append((p @ v[r // g], (top + total.log())[:, 0], p @ v[r // g].abs(), total,
+                    (q[:, r].double().abs() @ k[r // g].abs().t() * abs(scale)).amax(1)))
+    return [torch.stack(x, 1) for x in zip(*out)]
+
+
+def bound(o, a, z, v, n):
+    return 2.0 ** -8 * o.abs() + (2.0 ** -11 + 2.0 ** -13) * a + n * 2.0 ** -34 * v.abs().max() / z
+
+
+def check(q, cache, table, kv, n, scale):
+    k, v = kv
+    out, lse = fw.fp4_kv_attention(q, ints([0, len(q)]), ints([n]), table, cache, one(S_K), one(S_V),
+                                   len(q), scale, False, return_lse=True)
+    o, want_lse, a, z, reach = formula(q, k, v, scale)
+    d = (out.double() - o).abs()
+    lim = bound(o, a, z, v, n)
+    assert (d <= lim).all(), (d / lim).max()
+    d = (lse.double() - want_lse).abs()
+    assert (d <= 2.0 ** -19 * (reach + want_lse.abs() + 1)).all()
+    return o, a, z
+
+
+@pytest.mark.parametrize("gap", [10.0, 15.0, 16.3, 17.4, 20.0])
+@pytest.mark.parametrize("at", [0, -1])
+@pytest.mark.parametrize("rows,group", FORMS)
+@pytest.mark.parametrize("dim,n", [(64, 131072), (128, 20011)])
+def test_a_dominant_token_without_value(rows, group, at, gap, dim, n):
+    """The output is the tail alone, `gap` below the dominant token in the exponent;
+    found first, or last, when the tail's sums have to be scaled down."""
+    heads = 2
+    k = torch.zeros(n, heads, dim, device=DEV)
+    k[at, :, 5] = 1.0
+    v = (1 + 0.2 * torch.randn(n, heads, dim, generator=torch.Generator().manual_seed(int(gap)))).to(DEV)
+    v[at] = 0
+    cache, table, kv = stored(k.bfloat16(), v.bfloat16())
+    q = torch.zeros(rows, heads * group, dim, device=DEV)
+    q[:, :, 5] = 1.0
+    scale = gap / kv[0][0, at, 5].item()
+    scale = torch.tensor(scale, dtype=torch.float32).item()
+    o, _, _ = check(q.bfloat16(), cache, table, kv, n, scale)
+    assert (o > 0).all()
