@@ -1,5 +1,6 @@
 """How exact attention over the 4-bit cache is where many small weights make up
-the output: one dominant token whose V is 0 before a long uniform tail.
+the output: one dominant token whose V is 0 before a long uniform tail, and long
+contexts whose every 64 tokens show in some element of the output.
 
 Tolerances.  The weights are FP16 values of 2^(s - m + 9) (log2 units, m a running
 maximum no larger than the row's): half a step is 2^-11 of a weight from 2^-14 on,
@@ -18,12 +19,12 @@ import torch
 
 import fp8_w8a8_static_b200 as fw
 import _kv4
-from test_gpu_fp4_kv import DEV, S_K, S_V, ints, one
+from test_gpu_fp4_kv import DEV, S_K, S_V, ints, one, rand
 
 pytestmark = pytest.mark.gpu
 PAGE = 64
-# rows of the request, query heads of the K/V head: the few-rows kernel with 8 and
-# with 16 rows, the many-rows kernel (whose blocks share the tokens)
+# rows of the request, query heads of the K/V head: the few-rows kernel with 8, 16
+# and many rows, the many-rows kernel (whose blocks share the tokens)
 FORMS = [(1, 3), (6, 2), (300, 1), (1200, 1)]
 
 
@@ -91,3 +92,40 @@ def test_a_dominant_token_without_value(rows, group, at, gap, dim, n):
     scale = torch.tensor(scale, dtype=torch.float32).item()
     o, _, _ = check(q.bfloat16(), cache, table, kv, n, scale)
     assert (o > 0).all()
+
+
+@pytest.mark.parametrize("rows,group", FORMS)
+@pytest.mark.parametrize("dim,n", [(128, 4096), (128, 20000), (128, 65537), (64, 65537)])
+def test_every_chunk_of_a_long_context_counts(rows, group, dim, n):
+    """Element d of V is nonzero for the d-th run of the tokens alone, so 64 tokens
+    are a good part of some element: the bound tells every 64 tokens that are lost."""
+    heads = 2
+    t = torch.arange(n, device=DEV)
+    v = rand(n, heads, dim, seed=n).abs() + 0.5
+    v = v * (t[:, None, None] * dim // n == torch.arange(dim, device=DEV))
+    k = rand(n, heads, dim, seed=n + 1)
+    cache, table, kv = stored(k, v.to(torch.bfloat16))
+    q = rand(rows, heads * group, dim, seed=n + 2, scale=0.5)
+    scale = torch.tensor(dim ** -0.5, dtype=torch.float32).item()
+    o, a, z = check(q, cache, table, kv, n, scale)
+    lim = bound(o, a, z, kv[1], n)
+    chunks = -(-n // 64)
+    for r in range(heads * group):            # of the first row: what each chunk gives
+        w = torch.softmax(q[0, r].double() @ kv[0][r // group].t() * scale, 0)
+        part = w[:, None] * kv[1][r // group]
+        part = torch.nn.functional.pad(part, (0, 0, 0, chunks * 64 - n)).view(chunks, 64, dim).sum(1)
+        lost = (part > lim[0, r]).any(1)
+        assert lost[:n // 64].all()
+
+
+@pytest.mark.parametrize("n_free,used,wanted", [(4, 9, 3), (0, 5, 3), (4, 4, 3), (4, 2, 3)])
+def test_pool_when_more_is_used_than_there_is(n_free, used, wanted):
+    """pool = (used + taken, missing): where more is used than there are pages,
+    nothing is taken and used stays."""
+    free = torch.arange(100, 100 + n_free, dtype=torch.int32, device=DEV)
+    table = torch.full((2, 4), -1, dtype=torch.int32, device=DEV)
+    _, _, _, pool = fw.fp4_kv_tables(ints([0, 16]), ints([20, 1]), table, free, ints([used]), 16, 21)
+    taken = min(wanted, max(n_free - used, 0))
+    assert pool.tolist() == [used + taken, wanted - taken]
+    got = table[table >= 0].tolist()
+    assert got == list(range(100 + used, 100 + used + taken))
