@@ -343,6 +343,10 @@ __global__ void __launch_bounds__(THREADS) fp4_kv_tables_kernel(const TableArgs 
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int rank = blockIdx.x, ranks = gridDim.x;
   const int64_t used = max(0, *a.used);
+  const bool near = a.batch <= THREADS;  // one turn: the offsets are in shared memory
+  // lengths that the slots still need are replaced only after them (kv_lens - added
+  // would not do: kv_lens saturates)
+  const bool lens_later = !near && a.kv_lens == a.lens;
   int64_t rows = 0, pages = 0;  // of the requests before this turn
   for (int b0 = 0; b0 < a.batch; b0 += THREADS) {
     const int b = b0 + static_cast<int>(threadIdx.x);
@@ -386,7 +390,7 @@ __global__ void __launch_bounds__(THREADS) fp4_kv_tables_kernel(const TableArgs 
     s_old[threadIdx.x] = static_cast<int32_t>(old);
     if (rank == 0 && b < a.batch) {
       a.cu_q[b + 1] = saturate_i32(rows + r);
-      a.kv_lens[b] = saturate_i32(old + add);
+      if (!lens_later) a.kv_lens[b] = saturate_i32(old + add);
     }
     __syncthreads();
     const int here = min(THREADS, a.batch - b0);
@@ -414,7 +418,6 @@ __global__ void __launch_bounds__(THREADS) fp4_kv_tables_kernel(const TableArgs 
     }
   }
   cluster_sync();  // the entries and offsets above are visible to the whole cluster
-  const bool near = a.batch <= THREADS;  // the offsets are in shared memory
   const int32_t *cu = near ? s_cu : a.cu_q;
   const int last = min(a.n_slots, cu[a.batch]);  // slots behind have no token
   constexpr int RUN = 32 * kTableUnroll;
@@ -437,9 +440,8 @@ __global__ void __launch_bounds__(THREADS) fp4_kv_tables_kernel(const TableArgs 
       b[x] = b_first;
       if (i < end) {
         b[x] = request_of(cu, t0 + i, b_first, b_last);
-        // the request's new tokens are its last ones (lens may be kv_lens by now)
-        const int64_t old = near ? s_old[b[x]]
-                                 : a.kv_lens[b[x]] - static_cast<int64_t>(max(0, a.added[b[x]]));
+        // (lens may be kv_lens by now where there was one turn)
+        const int64_t old = near ? s_old[b[x]] : max(0, a.lens[b[x]]);
         at[x] = old + (t0 + i - cu[b[x]]);
       }
     }
@@ -455,6 +457,12 @@ __global__ void __launch_bounds__(THREADS) fp4_kv_tables_kernel(const TableArgs 
             page[x] < 0 ? -1
                         : (static_cast<int64_t>(page[x]) << a.page_shift) +
                               (at[x] & ((int64_t(1) << a.page_shift) - 1));
+  }
+  if (lens_later) {
+    cluster_sync();  // every block has read the lengths
+    if (rank == 0)
+      for (int b = threadIdx.x; b < a.batch; b += THREADS)
+        a.kv_lens[b] = saturate_i32(static_cast<int64_t>(max(0, a.lens[b])) + max(0, a.added[b]));
   }
 }
 
