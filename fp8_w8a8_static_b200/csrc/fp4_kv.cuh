@@ -331,7 +331,8 @@ __device__ __forceinline__ int request_of(const int32_t *cu, int t, int lo, int 
   return lo;
 }
 
-template <int THREADS>
+// NEAR: at most THREADS requests, one turn; the offsets stay in shared memory.
+template <int THREADS, bool NEAR>
 __global__ void __launch_bounds__(THREADS) fp4_kv_tables_kernel(const TableArgs a) {
   constexpr int WARPS = THREADS / 32;
   __shared__ int64_t warp_rows[WARPS], warp_pages[WARPS];
@@ -343,10 +344,9 @@ __global__ void __launch_bounds__(THREADS) fp4_kv_tables_kernel(const TableArgs 
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int rank = blockIdx.x, ranks = gridDim.x;
   const int64_t used = max(0, *a.used);
-  const bool near = a.batch <= THREADS;  // one turn: the offsets are in shared memory
   // lengths that the slots still need are replaced only after them (kv_lens - added
   // would not do: kv_lens saturates)
-  const bool lens_later = !near && a.kv_lens == a.lens;
+  const bool lens_later = !NEAR && a.kv_lens == a.lens;
   int64_t rows = 0, pages = 0;  // of the requests before this turn
   for (int b0 = 0; b0 < a.batch; b0 += THREADS) {
     const int b = b0 + static_cast<int>(threadIdx.x);
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(THREADS) fp4_kv_tables_kernel(const TableArgs 
     }
   }
   cluster_sync();  // the entries and offsets above are visible to the whole cluster
-  const int32_t *cu = near ? s_cu : a.cu_q;
+  const int32_t *cu = NEAR ? s_cu : a.cu_q;
   const int last = min(a.n_slots, cu[a.batch]);  // slots behind have no token
   constexpr int RUN = 32 * kTableUnroll;
   for (int64_t base = static_cast<int64_t>(rank * WARPS + warp) * RUN; base < a.n_slots;
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(THREADS) fp4_kv_tables_kernel(const TableArgs 
       if (i < end) {
         b[x] = request_of(cu, t0 + i, b_first, b_last);
         // (lens may be kv_lens by now where there was one turn)
-        const int64_t old = near ? s_old[b[x]] : max(0, a.lens[b[x]]);
+        const int64_t old = NEAR ? s_old[b[x]] : max(0, a.lens[b[x]]);
         at[x] = old + (t0 + i - cu[b[x]]);
       }
     }

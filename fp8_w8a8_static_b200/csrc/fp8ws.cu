@@ -1838,10 +1838,11 @@ int fp4_kv_tables(const int32_t *lens, const int32_t *added, int64_t batch, int 
   if (blocks > kTableMaxBlocks) blocks = kTableMaxBlocks;
   const int n = static_cast<int>(blocks);
   cudaStream_t st = as_stream(stream);
-  if ((few ? launch_ex(fp4_kv_tables_kernel<256>, dim3(n), dim3(256), 0, st, n, a)
-           : launch_ex(fp4_kv_tables_kernel<1024>, dim3(n), dim3(1024), 0, st, n, a)) !=
-      cudaSuccess)
-    return FP8WS_ERR_CUDA;
+  const cudaError_t e =
+      few             ? launch_ex(fp4_kv_tables_kernel<256, true>, dim3(n), dim3(256), 0, st, n, a)
+      : batch <= 1024 ? launch_ex(fp4_kv_tables_kernel<1024, true>, dim3(n), dim3(1024), 0, st, n, a)
+                      : launch_ex(fp4_kv_tables_kernel<1024, false>, dim3(n), dim3(1024), 0, st, n, a);
+  if (e != cudaSuccess) return FP8WS_ERR_CUDA;
   log_launch(kKindKvCache, lens, added, slots);
   return launch_status();
 }
