@@ -41,7 +41,7 @@ __all__ = [
     "fp8_check_shared_input_scale", "fp8_absmax_bf16", "fp8_silu_mul_absmax",
     "fp8_observer_scale", "fp8_rtn_quantize_weight",
     "device_check", "device_status", "launch_count", "launch_log", "launch_log_clear",
-    "split_plan", "gemm_plan",
+    "split_plan", "gemm_plan", "kv_attention_plan",
     "selftest_bounded_wait", "SITE_SELFTEST",
     "FP8", "OBSERVER_CONSTANT", "EXPORTED_SYMBOLS",
 ]
@@ -197,6 +197,9 @@ _SIGS = {
                                        ctypes.POINTER(ctypes.c_int)]),
     "fp8ws_split_plan": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int]
                          + [ctypes.POINTER(ctypes.c_int)] * 5),
+    "fp8ws_kv_attention_plan": (ctypes.c_int, [_I64, _I64, _I64, ctypes.c_int, _I64, _I64, _I64,
+                                               ctypes.c_int]
+                                + [ctypes.POINTER(ctypes.c_int)] * 3),
     "fp8ws_launch_count": (ctypes.c_int64, []),
     "fp8ws_launch_log": (ctypes.c_int, [ctypes.POINTER(LaunchRecord), ctypes.c_int]),
     "fp8ws_launch_log_clear": (None, []),
@@ -1187,6 +1190,18 @@ def split_plan(tiles: int, pairs: int, num_kb: int, scratch: bool = True) -> dic
                                    *[ctypes.byref(o) for o in out]), "fp8ws_split_plan")
     return dict(zip(("dp_tiles", "split_tiles", "splits", "kb_per_split", "halves"),
                     (o.value for o in out)))
+
+
+def kv_attention_plan(total_q: int, q_heads: int, kv_heads: int, head_dim: int, batch: int,
+                      max_q: int, tokens: int, sms: int = 148) -> dict:
+    """What fp4_kv_attention launches (host only), for tables that hold `tokens`
+    tokens a request: requests of up to few_rows rows go to the few-rows kernel,
+    the others to `blocks` 256-row blocks, each split `splits` ways."""
+    out = [ctypes.c_int() for _ in range(3)]
+    _check(load().fp8ws_kv_attention_plan(total_q, q_heads, kv_heads, head_dim, batch, max_q,
+                                          tokens, sms, *[ctypes.byref(o) for o in out]),
+           "fp8ws_kv_attention_plan")
+    return dict(zip(("few_rows", "blocks", "splits"), (o.value for o in out)))
 
 
 def launch_count() -> int:

@@ -1090,24 +1090,59 @@ int launch_kv_rows(DeviceInfo *d, KvAttnArgs a, cudaStream_t st) {
 // Which kernel takes a request's rows (tokens x query heads of a K/V head).
 // Timed on B200 (32 requests of 1024 tokens, 8 heads of 128): 16 rows 27 us by
 // fp4_kv_rows_kernel and 44 by fp4_kv_tiles_kernel, 32 rows 39 and 44, 48 rows 50
-// and 44, 128 rows 109 and 45; 64-wide heads cross between 48 and 64 rows.  With a
-// handful of 256-row blocks in all, the GPU is idle even with their splits (one
-// head, 8192 tokens: 128 rows 21.4 and 21.5 us, 256 rows 20.9 and 28.0).
+// and 44, 128 rows 109 and 45; 64-wide heads cross between 48 and 64 rows.
 constexpr int kKvFewRows = 40;
-constexpr int kKvFewItems = 4;
+// With a handful of 256-row blocks in all, the second kernel leaves most of the GPU
+// idle or splits the tokens thin, and the first one's cost is its 16-row tiles (of
+// all heads and requests) times the tokens, so it takes them all where the tiles are
+// few for the tokens that the tables can hold.  One head of 128, us of the first and
+// the second:
+//                 2048 tokens    8192      32768     131072
+//      64 rows      13    15     20  19    33  33     49   86
+//     256 rows      15    21     21  25    36  41     98  100
+//     512 rows      16    21     25  25    55  43    177   79
+//    1016 rows      19    21     35  26    95  46    337   90
+// The line below runs between 512 and 1016 rows at 8192 tokens, 256 and 512 at
+// 131072; heads, or requests, count like rows.  A 64-wide head's tile costs 0.6 of
+// a 128-wide one's (1016 rows: 24 and 22 us at 8192, 214 and 81 at 131072).
+constexpr int64_t kKvFewItems = 4;
+constexpr int64_t kKvRowTiles = 14;       // for any number of tokens, and
+constexpr int64_t kKvRowChunks = 2600;    // row tiles x 64-token chunks more
 // Chunks of a split at least, by the longest request that the tables can hold.
 constexpr int64_t kKvSplitChunks = 8;
 
-// 256-row blocks there can be: one begun by each request of more than few_rows
-// rows beside the full ones.
-int64_t kv_tile_blocks(const KvAttnArgs &a) {
-  const int64_t rows = static_cast<int64_t>(a.total_q) * a.group;
-  const int64_t begun = rows / (a.few_rows + 1);
-  return a.cache.heads * (rows / kKvTileRows + (begun < a.batch ? begun : a.batch));
+// What fp4_kv_attention launches.
+struct KvPlan {
+  int few_rows;    // requests of up to this many rows are fp4_kv_rows_kernel's
+  int64_t blocks;  // 256-row blocks of fp4_kv_tiles_kernel, 0: not launched
+  int splits;      // of their tokens
+};
+
+// tokens: what a row of the tables can hold.
+KvPlan kv_plan(int64_t total_q, int64_t group, int64_t heads, int head_dim, int64_t batch,
+               int64_t max_q, int64_t tokens, int sms) {
+  const KvPlan all_few{INT_MAX, 0, 1};  // should a request have more than max_q rows, too
+  if (max_q * group <= kKvFewRows) return all_few;
+  const int few_rows = batch == 1 ? 0 : kKvFewRows;  // one request, one kernel
+  // one block begun by each request of more than few_rows rows beside the full ones
+  const int64_t rows = total_q * group;
+  const int64_t begun = rows / (few_rows + 1);
+  const int64_t blocks = heads * (rows / kKvTileRows + (begun < batch ? begun : batch));
+  const int64_t chunks = (tokens + kKvChunk - 1) / kKvChunk;
+  const int64_t row_tiles = heads * ((rows + 15) / 16);
+  if (blocks == 0 ||
+      (blocks <= kKvFewItems &&
+       row_tiles * chunks * head_dim <= (kKvRowTiles * chunks + kKvRowChunks) * 128))
+    return all_few;
+  const int64_t places = sms < kKvTileSlots ? sms : kKvTileSlots;
+  const int64_t longest = tokens / (kKvSplitChunks * kKvChunk);
+  int64_t splits = places / blocks;
+  if (splits > longest) splits = longest;
+  return KvPlan{few_rows, blocks, splits > 1 ? static_cast<int>(splits) : 1};
 }
 
 template <int D, int BIT>
-int launch_kv_tiles(DeviceInfo *d, KvAttnArgs a, cudaStream_t st) {
+int launch_kv_tiles(DeviceInfo *d, const KvAttnArgs &a, int64_t blocks, cudaStream_t st) {
   using C = KvTilesCfg<D>;
   auto kern = fp4_kv_tiles_kernel<D>;
   int rc = once_per_device(d, BIT, [&] {
@@ -1117,13 +1152,6 @@ int launch_kv_tiles(DeviceInfo *d, KvAttnArgs a, cudaStream_t st) {
                : FP8WS_ERR_CUDA;
   });
   if (rc) return rc;
-  const int64_t blocks = kv_tile_blocks(a);
-  if (blocks == 0) return FP8WS_OK;
-  const int64_t places = d->sms < kKvTileSlots ? d->sms : kKvTileSlots;
-  const int64_t longest = (a.width << a.cache.page_shift) / (kKvSplitChunks * kKvChunk);
-  int64_t splits = places / blocks;
-  if (splits > longest) splits = longest;
-  a.splits = splits > 1 ? static_cast<int>(splits) : 1;
   if (launch_ex(kern, dim3(static_cast<unsigned>(blocks * a.splits)), dim3(kKvTileThreads), C::SMEM,
                 st, 1, a, kWaitLimitNs) != cudaSuccess)
     return FP8WS_ERR_CUDA;
@@ -1939,22 +1967,24 @@ int fp4_kv_attention(const uint16_t *q, int64_t total_q, int64_t q_heads, int64_
   if (rc) return rc;
   if (total_q == 0 || batch == 0 || max_q == 0) return FP8WS_OK;
   const size_t part_bytes = round256(kKvPartFloats * sizeof(float));
-  KvAttnArgs a{q, static_cast<int>(total_q), static_cast<int>(batch),
-                     static_cast<int>(q_heads / kv_heads), cu_q, kv_lens, block_table, table_width,
+  const int64_t group = q_heads / kv_heads;
+  const KvPlan plan = kv_plan(total_q, group, kv_heads, head_dim, batch, max_q,
+                              table_width << page_shift(page_size), d->sms);
+  const KvAttnArgs a{q, static_cast<int>(total_q), static_cast<int>(batch),
+                     static_cast<int>(group), cu_q, kv_lens, block_table, table_width,
                      KvCache{const_cast<uint8_t *>(cache), num_pages, static_cast<int>(kv_heads),
                              page_shift(page_size)},
-                     s_k, s_v, scale, causal ? 1 : 0, 1, kKvFewRows, s_out, out, lse,
+                     s_k, s_v, scale, causal ? 1 : 0, plan.splits, plan.few_rows, s_out, out, lse,
                      static_cast<float *>(workspace),
                      reinterpret_cast<int4 *>(static_cast<uint8_t *>(workspace) + part_bytes)};
-  const int64_t most = max_q * (q_heads / kv_heads);  // rows of a request
   cudaStream_t st = as_stream(stream);
-  if (batch == 1) a.few_rows = 0;  // one request, one kernel
-  if (most > kKvFewRows && kv_tile_blocks(a) > kKvFewItems) {
-    rc = head_dim == 128 ? launch_kv_tiles<128, 40>(d, a, st) : launch_kv_tiles<64, 41>(d, a, st);
-    if (rc || batch == 1) return rc;
-  } else {
-    a.few_rows = INT_MAX;  // all of them, should one have more than max_q rows, too
+  if (plan.blocks) {
+    rc = head_dim == 128 ? launch_kv_tiles<128, 40>(d, a, plan.blocks, st)
+                         : launch_kv_tiles<64, 41>(d, a, plan.blocks, st);
+    if (rc) return rc;
   }
+  if (plan.few_rows == 0) return FP8WS_OK;
+  const int64_t most = max_q * group;  // rows of a request
   if (head_dim == 128)
     return most <= 8 ? launch_kv_rows<128, 1, 32>(d, a, st) : launch_kv_rows<128, 2, 33>(d, a, st);
   return most <= 8 ? launch_kv_rows<64, 1, 34>(d, a, st) : launch_kv_rows<64, 2, 35>(d, a, st);
@@ -2129,6 +2159,23 @@ int fp8ws_split_plan(int tiles, int pairs, int num_kb, int has_scratch, int *dp_
   *splits = p.splits;
   *kb_per_split = p.kb_per_split;
   *halves = p.halves;
+  return FP8WS_OK;
+}
+
+int fp8ws_kv_attention_plan(int64_t total_q, int64_t q_heads, int64_t kv_heads, int head_dim,
+                            int64_t batch, int64_t max_q, int64_t tokens, int sms, int *few_rows,
+                            int *blocks, int *splits) {
+  if (!few_rows || !blocks || !splits) return FP8WS_ERR_NULL;
+  if (total_q < 0 || q_heads < 1 || q_heads > 65535 || kv_heads < 1 || q_heads % kv_heads != 0 ||
+      (head_dim != 64 && head_dim != 128) || batch < 0 || batch >= kLim31 || max_q < 0 ||
+      tokens < 0 || tokens >= kLim31 || sms < 1 || total_q >= kLim31 ||
+      total_q * q_heads >= kLim31 - 256)
+    return FP8WS_ERR_SHAPE;
+  const KvPlan p =
+      kv_plan(total_q, q_heads / kv_heads, kv_heads, head_dim, batch, max_q, tokens, sms);
+  *few_rows = p.few_rows;
+  *blocks = static_cast<int>(p.blocks);
+  *splits = p.splits;
   return FP8WS_OK;
 }
 

@@ -815,6 +815,19 @@ FP8WS_API int fp8ws_gemm_plan(int sms, int pairs, const int64_t *M, const int64_
 FP8WS_API int fp8ws_split_plan(int tiles, int pairs, int num_kb, int has_scratch, int *dp_tiles,
                                int *split_tiles, int *splits, int *kb_per_split, int *halves);
 
+/* What fp4_kv_attention launches for a shape, for tests and tuning; host only,
+ * touches no device.  tokens: what a row of the block table can hold; sms: the
+ * device's.  Requests of up to *few_rows rows (tokens x query heads of a K/V
+ * head) go to the few-rows kernel (2^31 - 1: all of them; 0: none, it is not
+ * launched), the others to *blocks blocks of up to 256 rows of the many-rows
+ * kernel (an upper bound on what the lengths on the device can need; 0: not
+ * launched), *splits thread blocks sharing the tokens of each.
+ * FP8WS_ERR_NULL for a NULL output, FP8WS_ERR_SHAPE for sizes that
+ * fp4_kv_attention refuses, or sms < 1. */
+FP8WS_API int fp8ws_kv_attention_plan(int64_t total_q, int64_t q_heads, int64_t kv_heads,
+                                      int head_dim, int64_t batch, int64_t max_q, int64_t tokens,
+                                      int sms, int *few_rows, int *blocks, int *splits);
+
 /* Launch log.  Every kernel the library enqueues is counted and recorded in a
  * small ring (the most recent FP8WS_LOG_CAPACITY records).  kind: 1 quant,
  * 2 GEMM, 3 SwiGLU-quant, 4 calibration, 5 fused gate/up SwiGLU-quant, 6 K/V
