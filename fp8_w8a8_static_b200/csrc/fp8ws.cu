@@ -1124,10 +1124,12 @@ KvPlan kv_plan(int64_t total_q, int64_t group, int64_t heads, int head_dim, int6
   const KvPlan all_few{INT_MAX, 0, 1};  // should a request have more than max_q rows, too
   if (max_q * group <= kKvFewRows) return all_few;
   const int few_rows = batch == 1 ? 0 : kKvFewRows;  // one request, one kernel
-  // one block begun by each request of more than few_rows rows beside the full ones
+  // n requests of more than few_rows rows each leave up to 255 places of their last
+  // block unused; their rows and those places are whole blocks
   const int64_t rows = total_q * group;
   const int64_t begun = rows / (few_rows + 1);
-  const int64_t blocks = heads * (rows / kKvTileRows + (begun < batch ? begun : batch));
+  const int64_t n = begun < batch ? begun : batch;
+  const int64_t blocks = heads * ((rows + (kKvTileRows - 1) * n) / kKvTileRows);
   const int64_t chunks = (tokens + kKvChunk - 1) / kKvChunk;
   const int64_t row_tiles = heads * ((rows + 15) / 16);
   if (blocks == 0 ||

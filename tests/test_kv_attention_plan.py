@@ -31,7 +31,7 @@ TIMED = [
     (256, 4, 131072, 1, 128, 338, 90), (128, 1, 32768, 1, 128, 30, 35), (512, 1, 32768, 1, 128, 55, 43),
     (1016, 1, 32768, 1, 128, 95, 46), (256, 1, 8192, 1, 128, 21, 25), (1016, 1, 8192, 1, 128, 35, 26),
     (1016, 1, 512, 1, 128, 14, 19), (256, 2, 2048, 1, 128, 16, 21), (512, 1, 131072, 2, 128, 337, 105),
-    (64, 1, 131072, 2, 128, 61, 69),
+    (64, 1, 131072, 2, 128, 61, 69), (256, 4, 512, 1, 128, 14, 19),
     (1016, 1, 131072, 1, 64, 214, 81), (256, 1, 131072, 1, 64, 63, 86), (512, 1, 8192, 1, 64, 18, 22),
     (128, 4, 131072, 1, 64, 113, 64),
 ]
@@ -62,6 +62,23 @@ def test_plans_hold_what_there_is(tokens, rows, heads, batch):
         assert p["blocks"] >= batch * heads * -(-rows // 256)
         assert p["splits"] == 1 or p["blocks"] * p["splits"] <= 148
         assert 1 <= p["splits"] <= max(1, tokens // 512)
+
+
+@pytest.mark.parametrize("heads", [1, 3, 8])
+@pytest.mark.parametrize("rows", [256, 255, 257, 512, 768, 5000, 5120])
+def test_one_request_has_no_block_too_many(rows, heads):
+    p = fw.kv_attention_plan(rows, heads, heads, 128, 1, rows, 131072)
+    if p["blocks"]:
+        assert p["blocks"] == heads * -(-rows // 256)
+        assert p["splits"] == max(1, 148 // p["blocks"])
+
+
+def test_blocks_of_several_requests_are_a_bound_for_any_lengths():
+    """Requests of any rows up to max_q with the same sum."""
+    for rows in ([256, 256], [300, 300, 40], [41, 41, 41, 41], [1, 1, 1, 700], [512] * 5, [257] * 3):
+        p = fw.kv_attention_plan(sum(rows), 8, 8, 128, len(rows), max(rows), 4096)
+        assert p["blocks"] >= 8 * sum(-(-r // 256) for r in rows if r > 40)
+        assert p["blocks"] < 8 * (sum(rows) / 256 + len(rows))
 
 
 def test_refusals():
