@@ -1113,6 +1113,7 @@ constexpr int64_t kKvSplitChunks = 8;
 
 // What fp4_kv_attention launches.
 struct KvPlan {
+  int64_t most;    // rows of a request
   int few_rows;    // requests of up to this many rows are fp4_kv_rows_kernel's
   int64_t blocks;  // 256-row blocks of fp4_kv_tiles_kernel, 0: not launched
   int splits;      // of their tokens
@@ -1121,8 +1122,10 @@ struct KvPlan {
 // tokens: what a row of the tables can hold.
 KvPlan kv_plan(int64_t total_q, int64_t group, int64_t heads, int head_dim, int64_t batch,
                int64_t max_q, int64_t tokens, int sms) {
-  const KvPlan all_few{INT_MAX, 0, 1};  // should a request have more than max_q rows, too
-  if (max_q * group <= kKvFewRows) return all_few;
+  // (max_q may be anything above, a captured graph's bound, say)
+  const int64_t most = (max_q < total_q ? max_q : total_q) * group;
+  const KvPlan all_few{most, INT_MAX, 0, 1};  // should a request have more than max_q rows, too
+  if (most <= kKvFewRows) return all_few;
   const int few_rows = batch == 1 ? 0 : kKvFewRows;  // one request, one kernel
   // n requests of more than few_rows rows each leave up to 255 places of their last
   // block unused; their rows and those places are whole blocks
@@ -1140,7 +1143,7 @@ KvPlan kv_plan(int64_t total_q, int64_t group, int64_t heads, int head_dim, int6
   const int64_t longest = tokens / (kKvSplitChunks * kKvChunk);
   int64_t splits = places / blocks;
   if (splits > longest) splits = longest;
-  return KvPlan{few_rows, blocks, splits > 1 ? static_cast<int>(splits) : 1};
+  return KvPlan{most, few_rows, blocks, splits > 1 ? static_cast<int>(splits) : 1};
 }
 
 template <int D, int BIT>
@@ -1986,10 +1989,10 @@ int fp4_kv_attention(const uint16_t *q, int64_t total_q, int64_t q_heads, int64_
     if (rc) return rc;
   }
   if (plan.few_rows == 0) return FP8WS_OK;
-  const int64_t most = max_q * group;  // rows of a request
   if (head_dim == 128)
-    return most <= 8 ? launch_kv_rows<128, 1, 32>(d, a, st) : launch_kv_rows<128, 2, 33>(d, a, st);
-  return most <= 8 ? launch_kv_rows<64, 1, 34>(d, a, st) : launch_kv_rows<64, 2, 35>(d, a, st);
+    return plan.most <= 8 ? launch_kv_rows<128, 1, 32>(d, a, st)
+                          : launch_kv_rows<128, 2, 33>(d, a, st);
+  return plan.most <= 8 ? launch_kv_rows<64, 1, 34>(d, a, st) : launch_kv_rows<64, 2, 35>(d, a, st);
 }
 
 int fp8_check_shared_input_scale(const float *const *d_scales, int n, void *stream) {

@@ -81,6 +81,15 @@ def test_blocks_of_several_requests_are_a_bound_for_any_lengths():
         assert p["blocks"] < 8 * (sum(rows) / 256 + len(rows))
 
 
+@pytest.mark.parametrize("max_q", [5, 64, 4096, 2 ** 31, 2 ** 62, 2 ** 63 - 1])
+@pytest.mark.parametrize("total_q,batch", [(5, 1), (5, 3), (64, 1), (64, 2)])
+def test_a_bound_above_the_rows_that_there_are_counts_as_those(total_q, batch, max_q):
+    p = fw.kv_attention_plan(total_q, 32, 8, 128, batch, max_q, 4096)
+    assert p == fw.kv_attention_plan(total_q, 32, 8, 128, batch, min(max_q, total_q), 4096)
+    if total_q == 5:  # 20 rows of a K/V head
+        assert p == dict(few_rows=ALL, blocks=0, splits=1)
+
+
 def test_refusals():
     ok = dict(total_q=4, q_heads=8, kv_heads=2, head_dim=64, batch=2, max_q=2, tokens=100)
     fw.kv_attention_plan(**ok)
