@@ -870,11 +870,11 @@ def _call(dev, fn, name, *args):
         raise FP8WSError(status, name)
 
 
-def _new(like, shape, dtype, stream):
-    """_empty on like's device."""
+def _new(like, stream):
+    """like.new_empty for a call on `stream` (see _empty)."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
-    return _empty(shape, dtype, like.device, stream)
+        return like.new_empty
+    return lambda shape, dtype=like.dtype: _empty(shape, dtype, like.device, stream)
 
 
 # ---------------------------------------- Linear with a fused epilogue
@@ -906,7 +906,7 @@ def fp8_linear_epilogue(xq, wq, s_in, s_w, bias=None, act="none", residual=None,
     dev, st = _on(xq, stream)
     bf16 = torch.bfloat16
     if out is None:
-        out = _new(xq, (M, N), bf16 if s_out is None else FP8, stream)
+        out = _new(xq, stream)((M, N), dtype=bf16 if s_out is None else FP8)
     _call(dev, lib.fp8_linear_epilogue, "fp8_linear_epilogue", _codes(xq, "xq", dev),
           _codes(wq, "wq", dev), M, N, K, _scalar(s_in, "s_in", dev), _scalar(s_w, "s_w", dev),
           None if bias is None else _ptr(bias, "bias", dev, bf16), kind,
@@ -958,8 +958,9 @@ def fp4_kv_tables(lens, added, block_table, free_pages, used, page_size: int, n_
     dev, st = _on(lens, stream)
     i32, i64 = torch.int32, torch.int64
     if out is None:
-        cu_q, kv_lens, pool = (_new(lens, n, i32, stream) for n in (B + 1, B, 2))
-        slots = _new(lens, n_slots, i64, stream)
+        new = _new(lens, stream)
+        cu_q, kv_lens, pool = new(B + 1), new(B), new(2)
+        slots = new(n_slots, dtype=i64)
         out = (cu_q, kv_lens, slots, pool)
     else:
         cu_q, kv_lens, slots, pool = out
@@ -1008,7 +1009,8 @@ def fp4_kv_gather(cache, slots, s_k, s_v, out=None, stream=None):
     dev, st = _on(cache, stream)
     bf16 = torch.bfloat16
     if out is None:
-        out = tuple(_new(cache, (T, heads, dim), bf16, stream) for _ in range(2))
+        new = _new(cache, stream)
+        out = new((T, heads, dim), dtype=bf16), new((T, heads, dim), dtype=bf16)
     k, v = out
     if k.numel() != T * heads * dim or v.numel() != T * heads * dim:
         raise ValueError(f"out must be two tensors [T, {heads}, {dim}]")
@@ -1052,12 +1054,14 @@ def fp4_kv_attention(q, cu_q, kv_lens, block_table, cache, s_k, s_v, max_q: int,
         raise ValueError("lse must be [total_q, q_heads]")
     dev, st = _on(q, stream)
     bf16, f32, i32, u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+    new = _new(q, stream)
     if workspace is None:
-        workspace = _workspace(_attention_workspace(), q.device, stream)
+        size = _attention_workspace()
+        workspace = new(size, dtype=u8) if stream is None else _workspace(size, q.device, stream)
     if out is None:
-        out = _new(q, shape, bf16 if s_out is None else FP8, stream)
+        out = new(shape, dtype=bf16 if s_out is None else FP8)
     if return_lse and lse is None:
-        lse = _new(q, shape[:2], f32, stream)
+        lse = new(shape[:2], dtype=f32)
     _call(dev, lib.fp4_kv_attention, "fp4_kv_attention", _ptr(q, "q", dev, bf16), shape[0],
           shape[1], B, _ptr(cu_q, "cu_q", dev, i32), _ptr(kv_lens, "kv_lens", dev, i32), max_q,
           _ptr(block_table, "block_table", dev, i32), table[1], _ptr(cache, "cache", dev, u8),
