@@ -358,7 +358,8 @@ __global__ void __launch_bounds__(kKvRowThreads, kv_blocks_per_sm(NT))
     const int rows = min(ROWS, req.q_len * a.group - row0);
 
     // Q of row 8n + g, this thread's elements, as FP16 of q 2^-e with 2^e the
-    // row's magnitude (exact but for elements below 2^-24 of the largest)
+    // row's magnitude: BF16 has 8 significant bits and FP16's smallest step is 2^-24,
+    // so it is exact down to 2^-17 of the largest and off by 2^-25 of it below
     uint32_t qf[NT][TILES][2];
     float cq[NT][2];  // 2^e c2 of this thread's two columns (rows 8n + 2t, + 1)
     int lim[NT][2];   // tokens that they see

@@ -672,8 +672,8 @@ FP8WS_API int fp4_kv_gather(const uint8_t *cache, int64_t num_pages, int page_si
  * A row that sees no token gives zeros, and lse -inf.  Rows before cu_q[0] and
  * behind cu_q[batch] (a padded batch) are left as they were.
  * Scores, maxima, sums and outputs are held in fp32; q enters the product as
- * FP16 times a power of two of its row (exact for elements above 2^-24 of the
- * row's largest), the cache's code * scale is exact in FP16, and the softmax
+ * FP16 times a power of two of its row (exact for elements above 2^-17 of the
+ * row's largest, off by at most 2^-25 of the largest below), the cache's code * scale is exact in FP16, and the softmax
  * weights are rounded to FP16 for the second product: by 2^-11 of a weight down to
  * 2^-23 of the row's largest, by 2^-34 of the largest below (a token whose score is 24
  * below the largest leaves the output, not lse).

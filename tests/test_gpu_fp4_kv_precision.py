@@ -118,6 +118,31 @@ def test_every_chunk_of_a_long_context_counts(rows, group, dim, n):
         assert lost[:n // 64].all()
 
 
+@pytest.mark.parametrize("rows,group", FORMS)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_small_query_elements_are_exact_down_to_2_17_of_the_largest(dim, rows, group):
+    """K is 0 where q's largest element is, so the scores are the small element's
+    products alone: every significand of it at 2^-17 shows in lse."""
+    n, heads = 700, 2
+    k = torch.zeros(n, heads, dim, device=DEV)
+    k[:, :, 5] = 1 + torch.arange(n, device=DEV)[:, None] % 7
+    cache, table, kv = stored(k.bfloat16(), rand(n, heads, dim, seed=4))
+    q = torch.zeros(rows, heads * group, dim, device=DEV)
+    q[:, :, 40] = 1.0
+    mantissa = torch.arange(rows * heads * group, device=DEV).view(rows, -1) * 37 % 128
+    q[:, :, 5] = 2.0 ** -17 * (1 + mantissa / 128)
+    check(q.bfloat16(), cache, table, kv, n, 2.0 ** 16)
+
+
+def test_what_fp16_holds_of_a_small_query_element():
+    """On its row's scale every BF16 significand is an FP16 value at 2^-17; at 2^-18
+    half of them are not, by half a step of 2^-24."""
+    x = 1 + torch.arange(128, dtype=torch.float64) / 128
+    assert torch.equal((x * 2.0 ** -17).half().double(), x * 2.0 ** -17)
+    off = ((x * 2.0 ** -18).half().double() - x * 2.0 ** -18).abs()
+    assert (off > 0).sum() == 64 and off.max() == 2.0 ** -25
+
+
 @pytest.mark.parametrize("n_free,used,wanted", [(4, 9, 3), (0, 5, 3), (4, 4, 3), (4, 2, 3)])
 def test_pool_when_more_is_used_than_there_is(n_free, used, wanted):
     """pool = (used + taken, missing): where more is used than there are pages,
