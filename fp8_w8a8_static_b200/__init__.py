@@ -886,8 +886,8 @@ def fp8_linear_epilogue(xq, wq, s_in, s_w, bias=None, act="none", residual=None,
                         out=None, stream=None) -> torch.Tensor:
     """act((s_in*s_w) * Xq . Wq^T + bias) + residual in one launch: BF16, or
     with s_out E4M3 codes of the value over s_out.  bias [N], residual [M,N]
-    BF16 (residual may be out); act: "none", "relu", "silu" or "gelu" (tanh
-    form)."""
+    BF16 (residual may be out); act: "none", "relu", "silu" or "gelu" (the tanh
+    form, not erf's)."""
     lib = load()
     a, b = xq.shape, wq.shape
     if len(a) != 2 or len(b) != 2 or a[1] != b[1]:

@@ -61,7 +61,9 @@ struct EpiCfg {
 // silu(x) = x / (1 + e^-x); gelu(x) = x / (1 + e^-2u) with u = sqrt(2/pi)
 // (x + 0.044715 x^3), the tanh form (0.5 (1 + tanh u) = 1 / (1 + e^-2u), which
 // keeps its relative accuracy where the value is small).  NaN passes through
-// all of them.
+// all of them.  The exponential's argument a is rounded, so the relative error
+// grows with it: |a| 2^-24 for each of its roundings (two of SiLU's, up to four of
+// GELU's, their constants' among them) beside some 2^-21 of ex2 and rcp.
 template <int ACT>
 __device__ __forceinline__ float activate(float x) {
   if constexpr (ACT == kActRelu) {

@@ -561,8 +561,10 @@ FP8WS_API int gated_mlp_per_token_fp8(const uint16_t *x, int64_t M, int64_t d, i
  *
  * all in fp32 up to the one rounding.  act: FP8WS_ACT_NONE, _RELU, _SILU
  * (x / (1 + e^-x)) or _GELU (the tanh form, 0.5 x (1 + tanh(sqrt(2/pi) (x +
- * 0.044715 x^3)))), with fast exponential and reciprocal (relative error of a
- * few 2^-22); a NaN passes through each of them.  An FP8 code may differ by
+ * 0.044715 x^3))), not the erf form), with fast exponential and reciprocal: with e^a
+ * the exponential, the relative error is at most 2^-20 + |a| 2^-22, since a itself
+ * is rounded, and a result is 0 where 1 + e^a exceeds 2^126 (x below about -87 for
+ * SiLU, -10 for GELU).  A NaN passes through each of them.  An FP8 code may differ by
  * one step from an exact evaluation's on values within rounding noise of a
  * code boundary.
  * bias: device [N] BF16, or NULL.  residual: device [M,N] BF16, row-major,
