@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kKvThreads, kKvBlocks)
 // for prompts).  The row offsets are searched in shared memory where one round
 // covers the batch.  All of it is latency, not bytes: dependent reads and the
 // instructions of a few SMs are what it counts (300 prompts, 80 thousand
-// tokens: 12.9 us, 36 with a full search per slot and one block filling the
+// tokens: 12.7 us, 36 with a full search per slot and one block filling the
 // pages; 32 requests of one token: 3.4 us).
 constexpr int kTableMaxBlocks = 8;  // the portable cluster size
 constexpr int kTableUnroll = 8;     // slots of a thread in flight
