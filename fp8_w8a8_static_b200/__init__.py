@@ -276,25 +276,51 @@ def _device_of(t: torch.Tensor):
     return torch.cuda.device(t.device)
 
 
-def _allocating_on(stream, device):
-    """Makes a call's stream the current one for what the call allocates.  The
-    caching allocator hands out memory of the current stream that earlier work
-    of that stream may still use, which only that stream is ordered behind."""
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = int(stream)  # 1: the legacy default stream's other handle
-        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=device)
-    return torch.cuda.stream(stream)
+def _side_stream(stream, device):
+    """A call's stream for what the call allocates, None where that is the
+    current one.  The caching allocator hands out memory of the current stream
+    that earlier work of that stream may still use, which only that stream is
+    ordered behind."""
+    if stream is None or device.type != "cuda":
+        return None
+    handle = _stream(stream)
+    if handle == 1:  # the legacy default stream's other handle
+        handle = 0
+    if handle == torch._C._cuda_getCurrentRawStream(device.index):
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(handle, device=device)
+
+
+def _on_side(side, make, shape, **how):
+    """make(shape, **how) with side the current stream."""
+    if side.device_index != torch._C._cuda_getDevice():
+        with torch.cuda.stream(side):
+            return make(shape, **how)
+    current, index, kind = torch._C._cuda_getCurrentStream(side.device_index)
+    torch.cuda.set_stream(side)
+    try:
+        return make(shape, **how)
+    finally:
+        torch._C._cuda_setStream(stream_id=current, device_index=index, device_type=kind)
+
+
+def _result(side, current, make, shape, **how):
+    """A result of a call on side.  It is the caller's, who reads it on the
+    current stream: freed, it is not handed out again before that work is done."""
+    t = _on_side(side, make, shape, **how)
+    t.record_stream(current)
+    return t
 
 
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
-    """A result of a call on `stream`.  It is the caller's, who reads it on the
-    current stream: freed, it is not handed out again before that work is done."""
-    if stream is None:
+    """torch.empty for a result of a call on `stream`."""
+    side = _side_stream(stream, device)
+    if side is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    with _allocating_on(stream, device):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(t.device))
-    return t
+    return _result(side, torch.cuda.current_stream(device), torch.empty, shape, dtype=dtype,
+                   device=device)
 
 
 # ---------------------------------------------------------------- hot path
@@ -375,10 +401,11 @@ def gated_mlp_static_fp8_workspace(M: int, d: int, I: int) -> int:
 
 def _workspace(nbytes: int, device, stream) -> torch.Tensor:
     # torch's caching allocator hands out 512-byte aligned blocks
-    if stream is None:
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-    with _allocating_on(stream, device):
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    nbytes = max(nbytes, 256)
+    side = _side_stream(stream, device)
+    if side is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _on_side(side, torch.empty, nbytes, dtype=torch.uint8, device=device)
 
 
 def gated_mlp_static_fp8(x, s_in, wg, s_wg, wu, s_wu, s_down, wd, s_wd, workspace=None, out=None,
@@ -871,10 +898,13 @@ def _call(dev, fn, name, *args):
 
 
 def _new(like, stream):
-    """like.new_empty for a call on `stream` (see _empty)."""
+    """like.new_empty for the results of a call on `stream`."""
     if stream is None:
         return like.new_empty
-    return lambda shape, dtype=like.dtype: _empty(shape, dtype, like.device, stream)
+    side = _side_stream(stream, like.device)
+    if side is None:
+        return like.new_empty
+    return functools.partial(_result, side, torch.cuda.current_stream(like.device), like.new_empty)
 
 
 # ---------------------------------------- Linear with a fused epilogue
